@@ -11,19 +11,25 @@ exception is raised.
 Path ("从 BF16 到 FP8：HunyuanVideo1.5推理优化复盘", section 三.1):
 BF16 activation -> dynamic per-token E4M3 quantisation -> FP8 GEMM against
 per-channel pre-quantised, K-major E4M3 weights -> scale / bias / bf16.
+
+Behind the Q / K / V projections: rotary positions with several axes
+(``rotary_axes``), a key / value cache in E4M3 with one power-of-two scale for
+each block of tokens and head (``KVCache``, ``kv_cache_append``) and attention
+over it (``kv_cache_attention``).
 """
 from __future__ import annotations
 
 import ctypes
 import os
-from typing import Dict, List, Optional, Sequence, Tuple
+from typing import Dict, List, NamedTuple, Optional, Sequence, Tuple, Union
 
 import torch
 
 __all__ = [
     "E4M3FN", "E5M2", "Fp8DitError", "FP8Linear", "library_path", "load_library",
     "quantize_rowwise", "act_quantize_rowwise", "quantize_weight_per_channel", "quantize_per_tensor", "convert_state_dict",
-    "scaled_linear_multi", "device_error", "selftest_expired_wait", "selftest_quotient", "as_float8",
+    "scaled_linear_multi", "rotary_frequencies", "rotary_axes", "KVCache", "kv_cache_append", "kv_cache_attention",
+    "device_error", "selftest_expired_wait", "selftest_quotient", "as_float8",
 ]
 
 E4M3FN = 0
@@ -32,7 +38,7 @@ _FORMAT_NAMES = {"float8_e4m3fn": E4M3FN, "e4m3fn": E4M3FN, "e4m3": E4M3FN,
                  "float8_e5m2": E5M2, "e5m2": E5M2, E4M3FN: E4M3FN, E5M2: E5M2}
 _TORCH_FP8 = {E4M3FN: torch.float8_e4m3fn, E5M2: torch.float8_e5m2}
 
-_STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED_SHAPE", 3: "EMPTY", 4: "CUDA", 5: "TIMEOUT"}
+_STATUS = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED_SHAPE", 3: "EMPTY", 4: "CUDA", 5: "TIMEOUT", 6: "INDEX"}
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _lib = None
@@ -51,6 +57,23 @@ def library_path() -> str:
 class _TensorDesc(ctypes.Structure):
     _fields_ = [("src", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dst", ctypes.c_void_p),
                 ("scale", ctypes.c_void_p), ("src_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _KvCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_blocks", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("block_tokens", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _KvBatch(ctypes.Structure):
+    _fields_ = [("block_table", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p), ("offsets", ctypes.c_void_p),
+                ("total_tokens", ctypes.c_int64), ("n_requests", ctypes.c_int32), ("table_width", ctypes.c_int32),
+                ("max_new", ctypes.c_int32), ("max_kv", ctypes.c_int32)]
 
 
 # Source element types of the per-tensor conversion (fp8dit_src_dtype).
@@ -92,6 +115,12 @@ def load_library():
     L.fp8_linear_set_host_pipeline.argtypes = [p, p, ctypes.c_size_t, i64, i32]
     L.fp8_scaled_linear_host.argtypes = [p, i64, p, p, p]
     L.fp8_linear_plan.argtypes = [p, i64, i32, ctypes.POINTER(i32), ctypes.POINTER(i32), ctypes.POINTER(i32)]
+    ph, pc, pb = ctypes.POINTER(_Heads), ctypes.POINTER(_KvCache), ctypes.POINTER(_KvBatch)
+    L.fp8_rotary_axes.argtypes = [ph, ph, ph, ph, i64, i32, p, st, p, ctypes.POINTER(i32), i32, i32, p]
+    L.fp8_kv_cache_append.argtypes = [pc, ph, ph, pb, p]
+    L.fp8_kv_cache_attention_workspace_size.argtypes = [pc, pb, i32]
+    L.fp8_kv_cache_attention_workspace_size.restype = ctypes.c_size_t
+    L.fp8_kv_cache_attention.argtypes = [pc, ph, pb, ph, p, ctypes.c_float, i32, p, ctypes.c_size_t, p]
     L.fp8dit_device_error.argtypes = [p]
     L.fp8dit_selftest_expired_wait.argtypes = [i64, p]
     L.fp8dit_selftest_quotient.argtypes = [p, p]
@@ -101,7 +130,8 @@ def load_library():
                  "fp8_linear_create", "fp8_linear_destroy", "fp8_scaled_linear", "fp8_scaled_linear_multi",
                  "fp8_scaled_linear_noalloc", "fp8_weight_only_linear", "fp8_scaled_linear_fused",
                  "fp8_linear_set_host_pipeline", "fp8_scaled_linear_host",
-                 "fp8_linear_plan", "fp8_linear_set_workspace", "fp8dit_device_error",
+                 "fp8_linear_plan", "fp8_linear_set_workspace", "fp8_rotary_axes", "fp8_kv_cache_append",
+                 "fp8_kv_cache_attention", "fp8dit_device_error",
                  "fp8dit_selftest_expired_wait",
                  "fp8dit_selftest_quotient"):
         getattr(L, name).restype = st
@@ -540,8 +570,200 @@ def scaled_linear_multi(layers: Sequence[FP8Linear], a: torch.Tensor,
     return list(ys)
 
 
+def _on_device(device: torch.device, fn, *args) -> int:
+    """Call a library entry with `device` as the current device."""
+    if device.index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+def _heads(x: torch.Tensor, name: str, dim: Optional[int], device: Optional[torch.device]) -> _Heads:
+    """[tokens, heads, dim] bf16 as the library sees it; any token and head
+    stride that is a multiple of 8 elements."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _BF16_DTYPES or x.dim() != 3:
+        raise ValueError(f"{name} must be a bf16 tensor [tokens, heads, dim]")
+    if not x.is_cuda or (device is not None and x.device != device):
+        raise ValueError(f"{name} must be on {device if device is not None else 'a CUDA device'} (got {x.device})")
+    n, h, d = x.shape
+    if dim is not None and d != dim:
+        raise ValueError(f"{name} must have heads of {dim} elements (got {d})")
+    s0, s1, s2 = x.stride()
+    if d > 1 and s2 != 1:
+        raise ValueError(f"{name}'s heads must be contiguous")
+    # The stride of an axis of one element says nothing: torch may report any.
+    return _Heads(x.data_ptr(), s0 if n > 1 else max(h, 1) * d, s1 if h > 1 else d, h, 0)
+
+
+_NO_HEADS = _Heads(None, 0, 0, 0, 0)
+
+
+def rotary_frequencies(axis_dims: Sequence[int], theta: float = 10000.0) -> torch.Tensor:
+    """The usual frequencies theta^(-2i / n) of each axis' n elements: float64
+    [sum(axis_dims) / 2] in host memory, in the order rotary_axes takes them."""
+    return torch.cat([float(theta) ** (-torch.arange(0, n, 2, dtype=torch.float64) / n) for n in axis_dims])
+
+
+def rotary_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor, freqs: torch.Tensor,
+                axis_dims: Sequence[int], interleaved: bool = True, q_out: Optional[torch.Tensor] = None,
+                k_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Rotary positions with several axes on q [M, heads, dim] and, if given, k
+    [M, kv heads, dim] (bf16, views of a merged projection included).
+
+    The first sum(axis_dims) elements of a head are pairs, (2i, 2i + 1) or with
+    interleaved=False (i, i + half); axis a owns the next axis_dims[a] / 2 of
+    them, and pair i of token m turns by positions[m, a] * freqs[i]. Later
+    elements are copied. positions: int32 or float32 [M, axes]; freqs: float64
+    in host memory (rotary_frequencies). q_out = q turns in place.
+    Returns (q_out, k_out).
+    """
+    M, _, dim = q.shape if q.dim() == 3 else (0, 0, 0)
+    hq = _heads(q, "q", None, None)
+    dev = q.device
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    elif q_out.shape != q.shape:
+        raise ValueError("q_out must have q's shape")
+    ho = hq if q_out is q else _heads(q_out, "q_out", dim, dev)
+    hk = hko = _NO_HEADS
+    if k is not None:
+        hk = _heads(k, "k", dim, dev)
+        if k.shape[0] != M:
+            raise ValueError("q and k must have the same number of tokens")
+        if k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+        elif k_out.shape != k.shape:
+            raise ValueError("k_out must have k's shape")
+        hko = hk if k_out is k else _heads(k_out, "k_out", dim, dev)
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    n = len(axis_dims)
+    if positions.dtype == torch.int32:
+        kind = 0
+    elif positions.dtype == torch.float32:
+        kind = 1
+    else:
+        raise ValueError(f"positions must be int32 or float32 (got {positions.dtype})")
+    if positions.shape != (M, n) or not positions.is_contiguous() or positions.device != dev:
+        raise ValueError(f"positions must be contiguous [{M}, {n}] on {dev}")
+    if (not isinstance(freqs, torch.Tensor) or freqs.dtype != torch.float64 or freqs.is_cuda or not freqs.is_contiguous()
+            or 2 * freqs.numel() != sum(axis_dims)):
+        raise ValueError(f"freqs must be contiguous float64 in host memory, {sum(axis_dims) // 2} of them")
+    _check(_on_device(dev, load_library().fp8_rotary_axes, hq, hk, ho, hko, M, dim, positions.data_ptr(), kind,
+                      freqs.data_ptr(), (ctypes.c_int32 * n)(*axis_dims), n, 1 if interleaved else 0, _stream(dev)))
+    return q_out, k_out
+
+
+class KVCache(NamedTuple):
+    """A key / value cache in E4M3FN: codes uint8 [blocks, kv heads, block
+    tokens, head dim] and one power-of-two scale, float32 [blocks, kv heads],
+    for each block of tokens and head. head dim is 64 or 128, a block 16, 32,
+    64 or 128 tokens."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    @classmethod
+    def empty(cls, n_blocks: int, block_tokens: int, kv_heads: int, head_dim: int = 128, device="cuda") -> "KVCache":
+        k = torch.empty((n_blocks, kv_heads, block_tokens, head_dim), dtype=torch.uint8, device=device)
+        s = torch.empty((n_blocks, kv_heads), dtype=torch.float32, device=device)
+        return cls(k, torch.empty_like(k), s, torch.empty_like(s))
+
+
+def _kv_cache(cache: Union[KVCache, Sequence[torch.Tensor]]) -> Tuple[_KvCache, torch.device]:
+    k, v, ks, vs = cache
+    if k.dim() != 4 or not k.is_cuda:
+        raise ValueError("the cache's codes must be [blocks, kv heads, block tokens, head dim] on a CUDA device")
+    dev, shape = k.device, k.shape
+    for t in (k, v):
+        if t.dtype not in (torch.uint8, torch.float8_e4m3fn) or t.shape != shape or not t.is_contiguous() or t.device != dev:
+            raise ValueError("the cache's k and v must be contiguous E4M3FN codes of one shape on one device")
+    for t in (ks, vs):
+        if t.dtype != torch.float32 or t.shape != shape[:2] or not t.is_contiguous() or t.device != dev:
+            raise ValueError("the cache's scales must be contiguous float32 [blocks, kv heads] beside its codes")
+    return _KvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), *(shape[i] for i in (0, 1, 2, 3))), dev
+
+
+def _kv_batch(block_table: torch.Tensor, kv_lens: torch.Tensor, offsets: torch.Tensor, total: int, max_new: int,
+              max_kv: Optional[int], block_tokens: int, dev: torch.device) -> _KvBatch:
+    n = kv_lens.numel()
+    for t, name, shape in ((block_table, "block_table", None), (kv_lens, "kv_lens", (n,)), (offsets, "offsets", (n + 1,))):
+        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev or (shape is not None and t.shape != shape):
+            raise ValueError(f"{name} must be contiguous int32 on {dev}, one row per request (offsets: one more)")
+    if block_table.dim() != 2 or block_table.shape[0] != n:
+        raise ValueError("block_table must be [requests, blocks per request]")
+    width = block_table.shape[1]
+    return _KvBatch(block_table.data_ptr(), kv_lens.data_ptr(), offsets.data_ptr(), total, n, width, max_new,
+                    width * block_tokens if max_kv is None else max_kv)
+
+
+def kv_cache_append(cache: Union[KVCache, Sequence[torch.Tensor]], k: torch.Tensor, v: torch.Tensor,
+                    block_table: torch.Tensor, kv_lens: torch.Tensor, offsets: torch.Tensor, max_new: int) -> None:
+    """Quantise the new tokens' keys and values [total, kv heads, dim] (bf16)
+    into the cache, in place.
+
+    Request b's new tokens are rows offsets[b] .. offsets[b + 1]; they become
+    the last ones of its kv_lens[b] tokens, token t in block block_table[b, t
+    // block tokens]. A block's scale grows with its tokens, its older codes
+    are brought along. block_table, kv_lens, offsets: int32 on the device
+    (a captured graph reads their values at each replay); max_new bounds the
+    new tokens of one request. A block may be written by one request only.
+    Rows past offsets[-1] are not read. Numbers outside their range are
+    skipped and reported by device_error() (INDEX).
+    """
+    c, dev = _kv_cache(cache)
+    hk, hv = _heads(k, "k", c.head_dim, dev), _heads(v, "v", c.head_dim, dev)
+    if k.shape != v.shape:
+        raise ValueError("k and v must have the same shape")
+    b = _kv_batch(block_table, kv_lens, offsets, k.shape[0], max_new, None, c.block_tokens, dev)
+    _check(_on_device(dev, load_library().fp8_kv_cache_append, c, hk, hv, b, _stream(dev)))
+
+
+def kv_cache_attention(q: torch.Tensor, cache: Union[KVCache, Sequence[torch.Tensor]], block_table: torch.Tensor,
+                       kv_lens: torch.Tensor, offsets: torch.Tensor, max_q: int, max_kv: Optional[int] = None,
+                       scale: Optional[float] = None, causal: int = 0, out: Optional[torch.Tensor] = None,
+                       return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Attention of the new tokens' queries q [total, heads, dim] (bf16) over
+    their requests' cached tokens; heads is a multiple of the cache's.
+
+    Arguments as for kv_cache_append; max_q bounds the new tokens of one
+    request and max_kv (default: the block table's width) kv_lens. scale
+    defaults to dim^-1/2. causal = 0: every query sees its request's kv_lens
+    tokens; causal = g: it sees the frames of g tokens up to its own whole
+    (1: the usual causal mask), the queries being the last tokens. A row that
+    sees nothing is 0. Returns out, or (out, lse) with the float32 [total,
+    heads] natural log-sum-exp. Rows past offsets[-1] are left as they are.
+    workspace: device scratch for split key ranges, allocated here if absent
+    (calls that overlap on the GPU must not share one).
+    """
+    c, dev = _kv_cache(cache)
+    hq = _heads(q, "q", c.head_dim, dev)
+    total, heads, dim = q.shape
+    b = _kv_batch(block_table, kv_lens, offsets, total, max_q, max_kv, c.block_tokens, dev)
+    if out is None:
+        out = torch.empty((total, heads, dim), dtype=torch.bfloat16, device=dev)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    ho = _heads(out, "out", dim, dev)
+    lse = torch.empty((total, heads), dtype=torch.float32, device=dev) if return_lse else None
+    L = load_library()
+    need = _on_device(dev, L.fp8_kv_cache_attention_workspace_size, c, b, heads)
+    if need and workspace is None:
+        workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _check(_on_device(dev, L.fp8_kv_cache_attention, c, hq, b, ho, None if lse is None else lse.data_ptr(),
+                      dim ** -0.5 if scale is None else scale, causal, ws, ws_bytes, _stream(dev)))
+    return (out, lse) if return_lse else out
+
+
 def device_error(device: Optional[torch.device] = None) -> int:
-    """Synchronise the current stream and read / clear the device error word (0 = OK, 5 = TIMEOUT)."""
+    """Synchronise the current stream and read / clear the device error word (0 = OK, 5 = TIMEOUT,
+    6 = INDEX: a length, offset or block index in device memory was outside its range)."""
     dev = device if device is not None else torch.device("cuda", torch.cuda.current_device())
     return int(load_library().fp8dit_device_error(_stream(dev)))
 

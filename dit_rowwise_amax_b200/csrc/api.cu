@@ -26,6 +26,8 @@ void set_error(const char* fmt, ...) {
     va_end(ap);
 }
 
+void clear_error() { t_last_error[0] = 0; }
+
 fp8dit_status cuda_fail(cudaError_t e, const char* what) {
     set_error("%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
     return FP8DIT_ERR_CUDA;
@@ -659,8 +661,12 @@ fp8dit_status fp8dit_device_error(fp8dit_stream_t stream) {
     if (word != 0) {
         if ((e = cudaMemset(dev->err_word, 0, sizeof(word))) != cudaSuccess)
             return cuda_fail(e, "clearing the device error word");
-        set_error("a bounded device wait expired (error word 0x%x)", word);
-        return FP8DIT_ERR_TIMEOUT;
+        if (word & kDevErrTimeout) {
+            set_error("a bounded device wait expired (error word 0x%x)", word);
+            return FP8DIT_ERR_TIMEOUT;
+        }
+        set_error("a length, offset or block index in device memory was outside its range (error word 0x%x)", word);
+        return FP8DIT_ERR_INDEX;
     }
     return FP8DIT_OK;
 }

@@ -17,6 +17,7 @@ namespace fp8dit {
 // Bits of the per-device error word.
 enum : uint32_t {
     kDevErrTimeout = 1u,
+    kDevErrIndex = 2u,  // a length, offset or block index in device memory outside its range
 };
 
 // Where a kernel reports an expired wait, and how long a wait may last.
@@ -38,6 +39,7 @@ struct DeviceInfo {
 // Returns nullptr (and sets the last error) on failure. Uses the current device.
 const DeviceInfo* device_info();
 void set_error(const char* fmt, ...);
+void clear_error();
 fp8dit_status cuda_fail(cudaError_t e, const char* what);
 
 // Reduction length K and CUDA device of a linear layer handle.

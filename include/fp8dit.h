@@ -35,12 +35,14 @@
  *    stream) and enqueue work only after every argument has been validated.
  *    An argument error returns a status and enqueues nothing. There is no
  *    fallback path: a shape the kernels cannot take is an error.
- *  - Device-side bounded waits that expire set a per-device error word;
- *    fp8dit_device_error() reads and clears it.
+ *  - Device-side bounded waits that expire, and lengths, offsets and block
+ *    indices in device memory that lie outside their range, set a per-device
+ *    error word; fp8dit_device_error() reads and clears it.
  *  - On any status other than FP8DIT_OK, fp8dit_last_error_string() (per
  *    thread) describes the failure.
  *  - CUDA graphs: the quantisers, the linear entry points (single, multi,
- *    weight-only, fused, stream-K) and the per-tensor conversion only enqueue
+ *    weight-only, fused, stream-K), the per-tensor conversion, the rotary
+ *    positions and the key / value cache's append and attention only enqueue
  *    kernels (and, per-tensor, a memset), so they can be captured into a
  *    graph and replayed; each replay reads whatever the captured buffers hold
  *    then. Make the first fp8_act_quantize_rowwise call on a device (it builds
@@ -65,7 +67,8 @@ typedef enum {
     FP8DIT_ERR_UNSUPPORTED_SHAPE = 2, /* K % 16 != 0, N % 8 != 0, size beyond the kernels' range */
     FP8DIT_ERR_EMPTY = 3,             /* per-tensor conversion with nothing to convert */
     FP8DIT_ERR_CUDA = 4,              /* a CUDA runtime / driver call failed */
-    FP8DIT_ERR_TIMEOUT = 5            /* a bounded device wait expired */
+    FP8DIT_ERR_TIMEOUT = 5,           /* a bounded device wait expired */
+    FP8DIT_ERR_INDEX = 6              /* a kernel met a length, offset or block index outside its range */
 } fp8dit_status;
 
 typedef enum { FP8DIT_E4M3FN = 0, FP8DIT_E5M2 = 1 } fp8dit_format;
@@ -375,10 +378,149 @@ fp8dit_status fp8_scaled_linear_multi(const fp8dit_linear* hs, int32_t n, int64_
 fp8dit_status fp8_linear_plan(fp8dit_linear h, int64_t M, int32_t n_problems, int32_t* block_m,
                               int32_t* block_n, int32_t* ctas);
 
+/* ------------------------------------------------------------ attention
+ * What follows the Q, K and V projections ("从 BF16 到 FP8", section 三.4)
+ * in a block: positions turned into q and k, k and v put into an 8-bit cache,
+ * and attention over that cache. The pages describe the projections only;
+ * these operators are defined here.
+ */
+
+#define FP8DIT_ROTARY_MAX_AXES 4
+#define FP8DIT_ROTARY_MAX_DIM 256
+
+typedef enum { FP8DIT_POS_I32 = 0, FP8DIT_POS_F32 = 1 } fp8dit_pos_dtype;
+
+/* One bf16 tensor [tokens, heads, dim] seen through its strides (in elements;
+ * the dim elements of a head are contiguous). Strides are multiples of 8 and
+ * at least dim, the pointer is 16-byte aligned. A view into a merged
+ * projection's output is one such tensor. */
+typedef struct {
+    uint16_t* ptr;
+    int64_t token_stride;
+    int64_t head_stride;
+    int32_t heads; /* 0: absent (ptr is not looked at) */
+    int32_t reserved;
+} fp8dit_heads;
+
+/*
+ * Rotary positions with several axes (time, height, width, ...) for q and k in
+ * one launch. The first R = sum(axis_dims) elements of every head are R / 2
+ * pairs; the pairs are dealt to the axes in order, axis_dims[a] / 2 to axis a.
+ * Pair i of token m turns by the angle positions[m, axis(i)] * freqs[i]:
+ *     (x, y) -> (x cos - y sin, x sin + y cos)
+ * with the pair at elements (2i, 2i + 1) (interleaved != 0) or (i, i + R / 2).
+ * Elements from R on are copied. The angle is taken in turns in double
+ * precision and reduced before its sine and cosine (fp32), so far positions
+ * lose nothing; the rotation is fp32, rounded once to bf16.
+ *   q, k            inputs [M, heads, dim]; k.heads may be 0.
+ *   q_out, k_out    outputs, same heads as their inputs. An output may be its
+ *                   own input (in place); any other overlap is an error of the caller.
+ *   positions       [M, n_axes] int32 or fp32 (pos_dtype), row-major, 4-byte aligned.
+ *   freqs           HOST array of R / 2 doubles, radians per unit of position.
+ *   axis_dims       HOST array of n_axes even positive numbers.
+ * Requires dim % 8 == 0, dim <= FP8DIT_ROTARY_MAX_DIM, n_axes <= FP8DIT_ROTARY_MAX_AXES, R <= dim, and for
+ * split halves R % 8 == 0. M == 0 is a no-op.
+ */
+fp8dit_status fp8_rotary_axes(const fp8dit_heads* q, const fp8dit_heads* k, const fp8dit_heads* q_out,
+                              const fp8dit_heads* k_out, int64_t M, int32_t dim, const void* positions,
+                              fp8dit_pos_dtype pos_dtype, const double* freqs, const int32_t* axis_dims,
+                              int32_t n_axes, int32_t interleaved, fp8dit_stream_t stream);
+
+/*
+ * A key / value cache in E4M3FN with one scale for each block of tokens and
+ * head. A block holds block_tokens consecutive tokens of one request.
+ *   k, v              codes [n_blocks, kv_heads, block_tokens, head_dim], contiguous, 16-byte aligned.
+ *   k_scale, v_scale  fp32 [n_blocks, kv_heads], contiguous; written before they are read.
+ * A scale is a power of two: S = 2^n with the smallest n >= -120 for which
+ * 448 S >= |x| for every x put into the block. E4M3 keeps its relative
+ * precision under any scale, and a power of two makes the quotient x / S, the
+ * change of scale when a later token of the block is larger, and code * S in
+ * bf16 (what the tensor cores multiply) exact, but for codes that the change
+ * of scale makes subnormal, which are rounded once more.
+ * head_dim is 64 or 128, block_tokens 16, 32, 64 or 128.
+ */
+typedef struct {
+    uint8_t* k;
+    uint8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int32_t n_blocks;
+    int32_t kv_heads;
+    int32_t block_tokens;
+    int32_t head_dim;
+} fp8dit_kv_cache;
+
+/*
+ * The requests of one call. Their new tokens lie one behind the other: those
+ * of request b are rows offsets[b] .. offsets[b + 1] of q, k, v and out, and
+ * are the last tokens of its kv_lens[b] tokens in the cache. Token t of
+ * request b is in block block_table[b, t / block_tokens] at t % block_tokens.
+ * All pointers are DEVICE pointers, so a captured graph reads the lengths of
+ * each replay.
+ *   block_table  int32 [n_requests, table_width], contiguous; entries past a request's length are not read.
+ *   kv_lens      int32 [n_requests]: tokens in the cache, the new ones included.
+ *   offsets      int32 [n_requests + 1], not decreasing, 0 <= offsets[b] <= total_tokens.
+ *                Rows from offsets[n_requests] on are neither read nor written.
+ *   max_new      bound of offsets[b + 1] - offsets[b]; it sets the launch's size.
+ *   max_kv       bound of kv_lens[b], at most table_width * block_tokens.
+ * A request whose numbers break these bounds is left out, and so is a token
+ * whose block index is not in 0 .. n_blocks - 1 (attention sees it as masked);
+ * both raise FP8DIT_ERR_INDEX in fp8dit_device_error().
+ */
+typedef struct {
+    const int32_t* block_table;
+    const int32_t* kv_lens;
+    const int32_t* offsets;
+    int64_t total_tokens;
+    int32_t n_requests;
+    int32_t table_width;
+    int32_t max_new;
+    int32_t max_kv;
+} fp8dit_kv_batch;
+
+/*
+ * Put the new tokens' keys and values into the cache: request b's new tokens
+ * go to positions kv_lens[b] - (offsets[b + 1] - offsets[b]) .. kv_lens[b].
+ * For every block they reach, and head: the scale grows to what the new
+ * tokens need (a block with no older token of the request starts anew), the
+ * older codes are brought to the new scale, the new codes are
+ * RNEsat(x / S). Blocks that are not reached keep every bit.
+ *   k, v  bf16 [total_tokens, kv_heads, head_dim]; finite values.
+ * A block may be written by one request only (several may read it).
+ */
+fp8dit_status fp8_kv_cache_append(const fp8dit_kv_cache* cache, const fp8dit_heads* k, const fp8dit_heads* v,
+                                  const fp8dit_kv_batch* batch, fp8dit_stream_t stream);
+
+/*
+ * Attention of the new tokens' queries over their requests' cached tokens:
+ *     out[r, h] = sum_t p_t V_t,  p = softmax_t(scale q[r, h] . K_t),  t < limit(r)
+ * K_t, V_t = code * S of the head h / (q.heads / kv_heads). limit(r) is
+ * kv_lens[b], or with causal = g > 0 (frames of g tokens; g = 1 is the usual
+ * causal mask) min(kv_lens[b], (pos / g + 1) g) with pos the query's position
+ * in its request: every query sees the frames up to its own whole. A row that
+ * sees nothing is 0 (its lse -infinity). Scores, softmax sums and output are
+ * held in fp32; p is rounded to bf16 for the product with V, the output once
+ * to bf16.
+ *   q, out     bf16 [total_tokens, q heads, head_dim]; q.heads % kv_heads == 0;
+ *              out must not overlap the inputs.
+ *   lse        fp32 [total_tokens, q heads], contiguous: natural log of the sum of exp(scale q . K_t); or NULL.
+ *   scale      finite, > 0.
+ *   workspace  DEVICE scratch of at least fp8_kv_cache_attention_workspace_size(...) bytes, 16-byte aligned
+ *              (may be NULL when that is 0); its contents do not matter, calls that overlap must not share it.
+ * Few queries over many tokens: the tokens are split over CTAs and their
+ * partial results joined by a second launch; results do not depend on timing.
+ */
+size_t fp8_kv_cache_attention_workspace_size(const fp8dit_kv_cache* cache, const fp8dit_kv_batch* batch,
+                                             int32_t q_heads);
+fp8dit_status fp8_kv_cache_attention(const fp8dit_kv_cache* cache, const fp8dit_heads* q, const fp8dit_kv_batch* batch,
+                                     const fp8dit_heads* out, float* lse, float scale, int32_t causal,
+                                     void* workspace, size_t ws_bytes, fp8dit_stream_t stream);
+
 /*
  * Synchronise `stream`, then read and clear the current device's error word.
  * Returns FP8DIT_ERR_TIMEOUT if a bounded device wait expired since the last
- * read, FP8DIT_ERR_CUDA if the synchronisation failed, else FP8DIT_OK.
+ * read, else FP8DIT_ERR_INDEX if a kernel met an index outside its range,
+ * FP8DIT_ERR_CUDA if the synchronisation failed, else FP8DIT_OK.
  */
 fp8dit_status fp8dit_device_error(fp8dit_stream_t stream);
 
