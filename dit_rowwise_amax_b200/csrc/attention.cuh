@@ -72,9 +72,11 @@ struct KvAttnArgs {
 // How an attention call is cut; a function of host-side sizes only.
 struct KvAttnPlan {
     int32_t rows_per_tile, row_tiles, splits, chunk;
+    bool tensor;  // the tcgen05 kernel
     size_t ws_bytes;
 };
 KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads, int num_sms);
+cudaError_t launch_kv_attn_tiles(const KvAttnArgs& a, cudaStream_t stream);  // 256-row tiles, tcgen05
 cudaError_t launch_kv_attention(const KvAttnPlan& plan, KvAttnArgs& a, cudaStream_t stream);
 
 // ------------------------------------------------------------ device side

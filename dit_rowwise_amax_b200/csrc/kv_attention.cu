@@ -365,18 +365,22 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
 
 }  // namespace
 
-// Cutting a call: row tiles of 8 rows while a request has at most 8, else of
-// 16; then, while the CTAs would not fill the GPU (four per SM), the keys are
-// cut into ranges of at least 256.
+// Cutting a call: up to 16 rows per request go to kv_attn_rows (8 or 16 rows
+// per CTA), more to the tcgen05 kernel (256). Then, while the CTAs would not
+// fill the GPU (four per SM, or one), the keys are cut into ranges of at least
+// 256 (512).
 KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads, int num_sms) {
     KvAttnPlan p{};
     const int64_t rows = (int64_t)b.max_new * (q_heads / c.heads);
-    p.rows_per_tile = rows <= 8 ? 8 : 16;
+    p.tensor = rows > 16;
+    p.rows_per_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : 256;
     const int64_t tiles = (rows + p.rows_per_tile - 1) / p.rows_per_tile;
     p.row_tiles = (int32_t)(tiles < 1 ? 1 : tiles);
     const int64_t ctas = (int64_t)b.n * p.row_tiles * c.heads;
-    int64_t splits = (4ll * num_sms + ctas - 1) / ctas;
-    const int64_t most = (b.max_kv + 255) / 256;
+    const int64_t fill = p.tensor ? num_sms : 4ll * num_sms;
+    const int64_t least = p.tensor ? 512 : 256;
+    int64_t splits = fill / ctas;
+    const int64_t most = (b.max_kv + least - 1) / least;
     if (splits > most) splits = most;
     if (splits < 1) splits = 1;
     int64_t chunk = (b.max_kv + splits - 1) / splits;
@@ -392,7 +396,8 @@ KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads,
 template <int D>
 static cudaError_t launch_for(const KvAttnPlan& p, const KvAttnArgs& a, cudaStream_t stream) {
     const dim3 grid((unsigned)((int64_t)a.b.n * a.row_tiles * a.splits), (unsigned)a.c.heads);
-    cudaError_t e = p.rows_per_tile == 8
+    cudaError_t e = p.tensor ? launch_kv_attn_tiles(a, stream)
+                    : p.rows_per_tile == 8
                         ? launch_pdl(kv_attn_rows<D, 1>, grid, dim3(32 * kWarps), 0, stream, 1, a)
                         : launch_pdl(kv_attn_rows<D, 2>, grid, dim3(32 * kWarps), 0, stream, 1, a);
     if (e != cudaSuccess || a.splits == 1) return e;

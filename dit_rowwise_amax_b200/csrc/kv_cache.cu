@@ -4,7 +4,7 @@
 // Per (block, head): amax over the new tokens, S = 2^n with the smallest n >=
 // -120 such that amax <= 448 S; a block that already holds tokens of its
 // request keeps the larger of its scale and S and, when it grows, has its
-// older codes brought over; the new codes are RNEsat(x / S), an exact product
+// other codes brought over; the new codes are RNEsat(x / S), an exact product
 // with 2^-n followed by one rounding.
 //
 // Bound: HBM, 2 bytes read and 1 written per element. One CTA owns one block
@@ -89,7 +89,8 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const __grid_constant__ 
         if (n != n_old) {
             // ratio = 2^(n_old - n): below 2^-126 every code becomes a zero anyway.
             const float ratio = n_old - n < -126 ? 0.0f : pow2(n_old - n);
-            for (int at = threadIdx.x; at < lo * VPR; at += blockDim.x) {
+            for (int at = threadIdx.x; at < T * VPR; at += blockDim.x) {
+                if (at >= lo * VPR && at < hi * VPR) continue;  // the new rows
                 uint2* p = reinterpret_cast<uint2*>(codes) + at;
                 uint2 w = *p;
                 uint32_t* ww = &w.x;

@@ -482,9 +482,10 @@ typedef struct {
  * Put the new tokens' keys and values into the cache: request b's new tokens
  * go to positions kv_lens[b] - (offsets[b + 1] - offsets[b]) .. kv_lens[b].
  * For every block they reach, and head: the scale grows to what the new
- * tokens need (a block with no older token of the request starts anew), the
- * older codes are brought to the new scale, the new codes are
- * RNEsat(x / S). Blocks that are not reached keep every bit.
+ * tokens need (a block with no older token of the request starts anew), when
+ * it grows the block's other codes, older tokens' and unused rows', are
+ * brought to the new scale, and the new codes are RNEsat(x / S). Blocks that
+ * are not reached keep every bit.
  *   k, v  bf16 [total_tokens, kv_heads, head_dim]; finite values.
  * A block may be written by one request only (several may read it).
  */

@@ -54,6 +54,7 @@ def append(codes, scale, x, table, kv_lens, offsets):
     """New codes and scales after the append of x [total, heads, D] (all CPU)."""
     codes, scale = codes.clone(), scale.clone().double()
     t, values = codes.shape[2], e4m3_table()
+    assert not bool(((codes & 127) == 127).any()), "NaN codes: no reference"
     for b, n in enumerate(kv_lens):
         start = n - (offsets[b + 1] - offsets[b])
         for j in range(start // t, -(-n // t) if n > start else 0):
@@ -66,7 +67,7 @@ def append(codes, scale, x, table, kv_lens, offsets):
                     old = float(scale[page, h])
                     s = max(s, old)
                     if s != old:
-                        codes[page, h, :held] = encode_e4m3(values[codes[page, h, :held].long()] * (old / s))
+                        codes[page, h] = encode_e4m3(values[codes[page, h].long()] * (old / s))
                 codes[page, h, held: hi - j * t] = encode_e4m3(part / s)
                 scale[page, h] = s
     return codes, scale.float()

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import attention_reference as ref
-from test_gpu_kv_cache import ints, make_table, offsets_of, run_append
+from test_gpu_kv_cache import ints, make_table, offsets_of, run_append, zeroed
 
 pytestmark = pytest.mark.gpu
 
@@ -125,7 +125,7 @@ def test_scales_over_the_whole_range(new, exponent):
 def test_scores_far_apart(new):
     """Rows whose maximum keeps rising by much, or is reached by one key only."""
     heads, kv, dim, t, n = 1, 1, 64, 16, 400
-    cache = fp8.KVCache.empty(25, t, kv, dim)
+    cache = zeroed(25, t, kv, dim)
     k = torch.zeros((n, 1, dim), device="cuda")
     k[:, 0, 0] = torch.arange(n, device="cuda") / 4.0
     k[200, 0, 1] = 100.0
@@ -276,7 +276,7 @@ def test_projection_rotary_append_attention():
     steps = [(37, 12), (60, 60), (1, 1), (1, 0), (1, 1)]
     final = [sum(s[i] for s in steps) for i in range(2)]
     table, blocks = make_table(final, t)
-    cache = fp8.KVCache.empty(blocks, t, heads, dim)
+    cache = zeroed(blocks, t, heads, dim)
     mirror = [c.cpu().clone() for c in cache]
     lens = [0, 0]
     for new in steps:

@@ -12,6 +12,13 @@ fp8 = pytest.importorskip("dit_rowwise_amax_b200")
 OK, INDEX = 0, 6
 
 
+def zeroed(*args):
+    cache = fp8.KVCache.empty(*args)
+    for x in cache:
+        x.zero_()
+    return cache
+
+
 def make_table(lens, t, spare=2, seed=0):
     need = [-(-n // t) for n in lens]
     pages = torch.randperm(sum(need) + spare, generator=torch.Generator().manual_seed(seed)).tolist()
@@ -68,9 +75,10 @@ def test_append_steps(t, dim, heads, steps):
 
 def test_token_by_token_scale_growth():
     """One token at a time into one block, each larger than all before: the
-    older codes come along at every step."""
+    block's other codes, unused rows' too, come along at every step."""
     g = torch.Generator("cuda").manual_seed(1)
-    cache = fp8.KVCache.empty(3, 16, 2, 64)
+    cache = zeroed(3, 16, 2, 64)
+    cache.k.copy_(torch.arange(16 * 64, device="cuda").view(16, 64) % 127)
     for i in range(16):
         k = (rand((1, 2, 64), g, False).float() * 2.0 ** (i / 2 - 4)).bfloat16()
         v = (rand((1, 2, 64), g, False).float() * 2.0 ** (-i)).bfloat16()
@@ -88,7 +96,7 @@ def special_rows():
 def test_special_values_one_per_block():
     x = special_rows()[:, None, :]
     n = x.shape[0]
-    cache = fp8.KVCache.empty(n, 16, 1, 64)
+    cache = zeroed(n, 16, 1, 64)
     run_append(cache, x.contiguous(), x.flip(0).contiguous(), [[i] for i in range(n)], [1] * n, list(range(n + 1)), max_new=1)
 
 
@@ -96,7 +104,7 @@ def test_special_values_after_one_another():
     """Zero, subnormal and huge tokens in one block, one call and token by token."""
     x = special_rows()[:, None, :].contiguous()
     n = x.shape[0]
-    cache = fp8.KVCache.empty(2, 16, 1, 64)
+    cache = zeroed(2, 16, 1, 64)
     run_append(cache, x, x.flip(0).contiguous(), [[0]], [n], [0, n], max_new=n)
     for i in range(n):
         run_append(cache, x[i:i + 1], x[n - 1 - i:n - i], [[1]], [i + 1], [0, 1], max_new=1)
@@ -138,9 +146,7 @@ def test_graph_replay_reads_new_lengths():
     g = torch.Generator("cuda").manual_seed(3)
     h, d, t = 2, 128, 16
     table = [[3, 1, 0], [2, 5, 4]]
-    cache = fp8.KVCache.empty(6, t, h, d)
-    for x in cache:
-        x.fill_(0)
+    cache = zeroed(6, t, h, d)
     k, v = rand((2, h, d), g), rand((2, h, d), g)
     tab, lens, offs = ints(table), ints([1, 1]), ints([0, 1, 2])
     mirror = [c.clone() for c in cache]
