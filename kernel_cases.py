@@ -3,7 +3,8 @@ inputs, for profiling it on its own (for example under Nsight Compute):
 
     python kernel_cases.py weight_only_ffn_up --iters 4
 
-Cases (inputs from ``synth``, the same as the benchmark's):
+Cases (inputs from ``synth``, the same as the benchmark's; the attention
+operators' are random):
     quantize_ffn_up, quantize_ffn_down   rowwise E4M3 quantiser on the FFN activations
     quantize_hidden                      rowwise E4M3 quantiser on hidden_states [32760, 2048]
     gelu_quantize_ffn_down               GELU -> E4M3 producer on a [4096, 8192] activation
@@ -17,6 +18,12 @@ Cases (inputs from ``synth``, the same as the benchmark's):
     state_dict_e4m3fn, state_dict_e5m2   per-tensor conversion of the 192-tensor DiT weight set
     qkv_encoder                          Q/K/V projections of encoder_hidden_states [26, 2048]:
                                          one quantise + one grouped GEMM (128 x 64 tiles)
+    rotary_video                         rotary positions (16, 56, 56) on q and k of 32760 tokens, 16 heads of 128
+    append_video                         keys and values of 32760 tokens into the E4M3 cache
+    attend_batch                         one query token of each of 32 requests over 8000 cached tokens
+    attend_frame                         1560 query tokens over 32760 cached tokens, 16 heads
+    attend_frames_8heads                 4096 query tokens over 16384 cached tokens, 8 heads: 128 CTAs, one wave
+                                         (small enough for a multi-pass profile)
     state_dict_e4m3fn_4blocks            the same on the first 4 blocks' 24 tensors (400 MB of bf16,
                                          above L2; small enough for a multi-pass profile)
 Layer creation runs the per-channel weight quantiser first; every case then
@@ -34,13 +41,15 @@ import numpy as np  # noqa: E402
 import torch  # noqa: E402
 
 import synth  # noqa: E402
-from dit_rowwise_amax_b200 import (E4M3FN, E5M2, FP8Linear, act_quantize_rowwise, device_error,  # noqa: E402
-                                   quantize_per_tensor, quantize_rowwise, scaled_linear_multi)
+from dit_rowwise_amax_b200 import (E4M3FN, E5M2, FP8Linear, KVCache, act_quantize_rowwise, device_error,  # noqa: E402
+                                   kv_cache_append, kv_cache_attention, quantize_per_tensor, quantize_rowwise, rotary_axes,
+                                   rotary_frequencies, scaled_linear_multi)
 
 CASES = ("quantize_ffn_up", "quantize_ffn_down", "quantize_hidden", "gelu_quantize_ffn_down", "gemm_ffn_up", "gemm_ffn_down",
          "weight_only_ffn_up", "weight_only_ffn_down", "fused_ffn_up", "fused_ffn_down", "gemm_text_ffn_down",
          "split_k_text_ffn_down", "weight_only_text_ffn_down", "split_k_weight_only_text_ffn_down",
-         "state_dict_e4m3fn", "state_dict_e5m2", "state_dict_e4m3fn_4blocks", "qkv_encoder")
+         "state_dict_e4m3fn", "state_dict_e5m2", "state_dict_e4m3fn_4blocks", "qkv_encoder",
+         "rotary_video", "append_video", "attend_batch", "attend_frame", "attend_frames_8heads")
 STATE_DICT_4BLOCKS = 24  # tensors in the first four DiT blocks
 TEXT_TOKENS = 26  # encoder_hidden_states length
 
@@ -49,8 +58,42 @@ def _dev(a: np.ndarray, dev) -> torch.Tensor:
     return torch.from_numpy(np.ascontiguousarray(a).view(np.int16)).view(torch.bfloat16).to(dev)
 
 
+def run_attention(case: str, iters: int, dev) -> None:
+    """requests, query tokens, cached tokens, query heads, kv heads."""
+    n, nq, kv, heads, hk = {"rotary_video": (1, 32760, 32760, 16, 16), "append_video": (1, 32760, 32760, 16, 16),
+                            "attend_batch": (32, 1, 8000, 32, 8), "attend_frame": (1, 1560, 32760, 16, 16),
+                            "attend_frames_8heads": (1, 4096, 16384, 8, 8)}[case]
+    gen = torch.Generator(device=dev).manual_seed(0)
+    q = torch.randn((n * nq, heads, 128), generator=gen, device=dev).bfloat16()
+    if case == "rotary_video":
+        k, at = torch.randn_like(q), torch.arange(nq, device=dev)
+        pos, dims = torch.stack([at // 1560, at // 52 % 30, at % 52], 1).int(), (16, 56, 56)
+        freqs, qo, ko = rotary_frequencies(dims, 256.0), torch.empty_like(q), torch.empty_like(q)
+        for _ in range(iters):
+            rotary_axes(q, k, pos, freqs, dims, q_out=qo, k_out=ko)
+        return
+    width = (kv + 127) // 128
+    table = torch.randperm(n * width, generator=gen, device=dev).int().view(n, width)
+    cache = KVCache.empty(n * width, 128, hk, 128, dev)
+    x = torch.randn((n * kv, hk, 128), generator=gen, device=dev).bfloat16()
+    lens = torch.full((n,), kv, dtype=torch.int32, device=dev)
+    for _ in range(iters if case == "append_video" else 1):
+        kv_cache_append(cache, x, x, table, lens, torch.arange(0, n * kv + 1, kv, dtype=torch.int32, device=dev), max_new=kv)
+    if case == "append_video":
+        return
+    offsets, out = torch.arange(0, n * nq + 1, nq, dtype=torch.int32, device=dev), torch.empty_like(q)
+    for _ in range(iters):
+        kv_cache_attention(q, cache, table, lens, offsets, max_q=nq, max_kv=kv, out=out)
+
+
 def run(case: str, iters: int) -> None:
     dev = torch.device("cuda", 0)
+    if case in ("rotary_video", "append_video") or case.startswith("attend"):
+        run_attention(case, iters, dev)
+        torch.cuda.synchronize()
+        if device_error() != 0:
+            raise SystemExit(f"{case}: device error word set")
+        return
     if case.startswith("state_dict"):
         layout = synth.state_dict_layout()
         if case.endswith("_4blocks"):
