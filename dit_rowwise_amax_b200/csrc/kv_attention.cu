@@ -5,12 +5,12 @@
 // head; one CTA takes a tile of up to 16 rows, one kv head and one range of
 // keys, so a cached byte is read once for the whole group of heads. Its four
 // warps walk the range in granules of 16 keys (always inside one block: a
-// block is 16 tokens or more), each with its own running maximum, sum and
+// block is 16 tokens or more), each with its own running references, sums and
 // output, which are joined through shared memory at the end.
 //
-// Mathematics, per granule and warp (mma.sync m16n8k16, bf16 -> fp32):
+// Mathematics, per granule and warp (mma.sync m16n8k16, fp16 -> fp32):
 //     S^T = K Q^T      A = 16 keys x dim, B = 8 query rows per column tile
-//     P^T = 2^(S^T - m)
+//     P^T = 2^(t - m)  t = s + log2 S_V: the score plus V's block scale
 //     O^T += V^T P^T   A = dim x 16 keys, B = P^T
 // Keys and values are the A operands so that 8 rows fill a column tile (the
 // 16-row A side would be half empty at a group of 8 or fewer). Both products
@@ -18,19 +18,29 @@
 // loads straight from the cache as its fragments: for K the 16 bytes at
 // dim 16 tig (+ 64) of keys gid and gid + 8, with Q permuted the same way;
 // for V the 16 bytes at dim 16 gid of keys 2 tig, 2 tig + 1, 2 tig + 8,
-// 2 tig + 9, whose bytes are paired across keys by the permute that decodes
-// them. P^T comes out of S^T by an 8 x 8 transpose in registers (movmatrix).
-// Decoded codes are multiplied by 2^120 S, which is exact: the products are
-// those of q and of what the cache holds.
+// 2 tig + 9, whose bytes a permute pairs across keys. P^T comes out of S^T by
+// an 8 x 8 transpose in registers (movmatrix).
 //
-// The maximum is lazy: rows keep a reference m that only moves when a score
-// exceeds it by 8 (in log2 units), so the usual granule needs one vote and no
-// shuffles; p is at most 2^8.
+// Why fp16: an E4M3 code is exact in fp16 and one cvt turns two codes into
+// two fp16 (decoding to bf16 takes four instructions, and this kernel is bound
+// by issue slots before HBM if it does: 520 against 300 per granule). Neither
+// range is at risk: q is brought to 2^14 by a power of two per row, undone in
+// the score (its bits below 2^-24 of the row's largest are lost, as in any
+// fp32 sum); K's scale multiplies the score; V's is in the exponent of P, with
+// a reference m of its own, so P is 2^-25 exact relative to the row's largest
+// contribution however V's scales differ. The softmax sum takes a second
+// exponential 2^(s - mu) in fp32.
+//
+// Both references are lazy: they only move when a score exceeds them by 8
+// (log2 units), so the usual granule needs one vote and no shuffles; p is at
+// most 2^8.
 //
 // Bound: HBM, 2 bytes per token, kv head and dim; a granule's loads are issued
 // one granule ahead (4 KB in flight per warp at dim 128).
 #include "attention.cuh"
 #include "fp8_codec.cuh"
+
+#include <cuda_fp16.h>
 
 namespace fp8dit {
 namespace {
@@ -44,9 +54,19 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<uint32_t*>(&v);
 }
+__device__ __forceinline__ uint32_t pack2h(float lo, float hi) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+// Two E4M3 codes (low 16 bits) -> two fp16, exact.
+__device__ __forceinline__ uint32_t decode2(uint32_t codes) {
+    uint32_t d;
+    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(d) : "r"(codes));
+    return d;
+}
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -57,58 +77,213 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     return y;
 }
 
-// One granule's codes and scales as this lane needs them.
-template <int D>
-struct Granule {
-    uint32_t k[2][D / 16];  // keys gid, gid + 8: D / 16 words of 4 codes
-    uint32_t v[4][D / 32];  // keys 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9: D / 32 words
-    float ks, vs;
-    bool ok;  // its block index is valid
-};
+// A warp's ring of granules in shared memory, filled by cp.async two granules
+// ahead: 8 KB of loads in flight per warp (dim 128) without registers to hold
+// them. (One granule ahead in registers, the GPU waited on loads 60% of the
+// time: 4.2 TB/s.) 16-byte pieces are swizzled within 128-byte lines so that
+// the fragments' reads are free of bank conflicts.
+constexpr int kStages = 3;
 
 template <int D>
-__device__ __forceinline__ void load_granule(Granule<D>& g, const KvAttnArgs& a, int page, int head, int row, int gid,
-                                             int tig) {
-    g.ok = page >= 0 && page < a.c.n_blocks;
-    if (!g.ok) {
-        if ((threadIdx.x & 31) == 0) atomicOr(a.err.word, kDevErrIndex);
-        page = 0;
+struct Ring {
+    static constexpr int BYTES = kGranule * D;  // a granule's K or V codes
+    uint8_t k[kStages][BYTES], v[kStages][BYTES];
+};
+struct Header {
+    float ks, vs;
+    int ok;  // the block index is valid
+    int pad;
+};
+
+// Byte offset of 16-byte piece c of a granule's row r.
+template <int D>
+__device__ __forceinline__ int piece(int r, int c) {
+    const int line = D == 128 ? r : r >> 1;
+    const int p = D == 128 ? c : (r & 1) * 4 + c;
+    // K's reads pair rows 2 i, 2 i + 1; V's take rows 0, 2, 4, 6 (+ 1) at once.
+    const int sw = D == 128 ? (((r ^ (r >> 2)) & 1) << 2) | (r & 2) : (line & 3) << 1;
+    return line * 128 + ((p ^ sw) << 4);
+}
+
+__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int D>
+__device__ __forceinline__ void load_granule(Ring<D>& ring, Header* hdr, int stage, const KvAttnArgs& a, int page,
+                                             int head, int row, int lane) {
+    const bool ok = page >= 0 && page < a.c.n_blocks;
+    if (lane == 0) {
+        hdr[stage].ok = ok;
+        if (!ok) atomicOr(a.err.word, kDevErrIndex);
     }
+    if (!ok) return;
     const int64_t slot = (int64_t)page * a.c.heads + head;
-    const int64_t at = ((slot << a.c.block_log2) + row) * D;
-    g.ks = a.c.ks[slot];
-    g.vs = a.c.vs[slot];
-    const uint8_t* kp = a.c.k + at + tig * 16;
+    const int64_t at = ((slot << a.c.block_log2) + row) * D + lane * 16;
+    constexpr int kPieces = D / 16;  // per row
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int h = 0; h < D / 64; ++h) {
-            const uint4 w = *reinterpret_cast<const uint4*>(kp + (gid + 8 * r) * D + 64 * h);
-            g.k[r][4 * h] = w.x, g.k[r][4 * h + 1] = w.y, g.k[r][4 * h + 2] = w.z, g.k[r][4 * h + 3] = w.w;
-        }
-    const uint8_t* vp = a.c.v + at + gid * (D / 8);
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const uint8_t* p = vp + (2 * tig + (r & 1) + 8 * (r >> 1)) * D;
-        if (D == 128) {
-            const uint4 w = *reinterpret_cast<const uint4*>(p);
-            g.v[r][0] = w.x, g.v[r][1] = w.y, g.v[r][D / 32 - 2] = w.z, g.v[r][D / 32 - 1] = w.w;
-        } else {
-            const uint2 w = *reinterpret_cast<const uint2*>(p);
-            g.v[r][0] = w.x, g.v[r][1] = w.y;
-        }
+    for (int i = 0; i < kGranule * kPieces / 32; ++i) {
+        const int p = i * 32 + lane;
+        const int to = piece<D>(p / kPieces, p % kPieces);
+        cp_async16(ring.k[stage] + to, a.c.k + at + i * 512);
+        cp_async16(ring.v[stage] + to, a.c.v + at + i * 512);
     }
+    if (lane == 0) cp_async4(&hdr[stage].ks, a.c.ks + slot);
+    if (lane == 1) cp_async4(&hdr[stage].vs, a.c.vs + slot);
 }
 
 template <int D, int NT>
 struct RowsSmem {
-    float m[kWarps][8 * NT], l[kWarps][8 * NT];
+    float m[kWarps][8 * NT], mu[kWarps][8 * NT], l[kWarps][8 * NT];
     float o[kWarps][8 * NT][D + 4];
 };
 
+// A warp's running state: per lane the columns (query rows) 2 tig, 2 tig + 1 of
+// every column tile.
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kWarps) kv_attn_rows(const __grid_constant__ KvAttnArgs a) {
-    __shared__ RowsSmem<D, NT> sm;
+struct RowsState {
+    uint32_t q[NT][D / 16][2];  // scaled fp16 Q^T fragments
+    float cq[NT][2];            // softmax scale * log2(e) / q's scale
+    int limit[NT][2];           // keys the row sees
+    float m[NT][2], mu[NT][2], l[NT][2], o[NT][D / 16][4];
+};
+
+template <int D, int NT>
+__device__ __forceinline__ void attend_granule(RowsState<D, NT>& st, const uint8_t* kc, const uint8_t* vc,
+                                               const Header& h, int key, int least, int len, int gid, int tig) {
+    if (!h.ok) return;
+    const float ks = h.ks, vs = h.vs;
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+        const uint4 x4 = *reinterpret_cast<const uint4*>(kc + piece<D>(gid, 4 * c + tig));
+        const uint4 y4 = *reinterpret_cast<const uint4*>(kc + piece<D>(gid + 8, 4 * c + tig));
+        const uint32_t x[4] = {x4.x, x4.y, x4.z, x4.w}, y[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a0 = decode2(x[i]), a1 = decode2(y[i]), a2 = decode2(x[i] >> 16), a3 = decode2(y[i] >> 16);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma_16816(s[nt], a0, a1, a2, a3, st.q[nt][4 * c + i][0], st.q[nt][4 * c + i][1]);
+        }
+    }
+    // V's codes: keys 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9, D / 8 dims from gid (D / 8).
+    uint32_t v[4][D / 32];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int row = 2 * tig + (r & 1) + 8 * (r >> 1);
+        if (D == 128) {
+            const uint4 w = *reinterpret_cast<const uint4*>(vc + piece<D>(row, gid));
+            v[r][0] = w.x, v[r][1] = w.y, v[r][D / 32 - 2] = w.z, v[r][D / 32 - 1] = w.w;
+        } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(vc + piece<D>(row, gid >> 1) + (gid & 1) * 8);
+            v[r][0] = w.x, v[r][1] = w.y;
+        }
+    }
+    // V's scale is a power of two: its log2 is its exponent.
+    const float ev = (float)((int)(__float_as_uint(vs) >> 23) - 127);
+    bool over = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const float f0 = st.cq[nt][0] * ks, f1 = st.cq[nt][1] * ks;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[nt][i] *= i & 1 ? f1 : f0;
+    }
+    if (key + kGranule > least) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (key + gid + 8 * (i >> 1) >= st.limit[nt][i & 1]) s[nt][i] = kNegInf;
+        // Rows behind the last token may hold NaN codes, which a p of 0 keeps.
+        if (key + kGranule > len) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (key + 2 * tig + (r & 1) + 8 * (r >> 1) >= len) {
+#pragma unroll
+                    for (int w = 0; w < D / 32; ++w) v[r][w] = 0;
+                }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float t = fmaxf(s[nt][i], s[nt][i + 2]);
+            over |= t > st.mu[nt][i] + kLazy || t + ev > st.m[nt][i] + kLazy;
+        }
+    if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float t = fmaxf(s[nt][i], s[nt][i + 2]);
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                const float mu = fmaxf(st.mu[nt][i], t), m = fmaxf(st.m[nt][i], t + ev);
+                st.l[nt][i] *= mu == kNegInf ? 1.0f : ex2_approx(st.mu[nt][i] - mu);
+                const float c = m == kNegInf ? 1.0f : ex2_approx(st.m[nt][i] - m);
+                st.mu[nt][i] = mu;
+                st.m[nt][i] = m;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                    st.o[nt][d][i] *= c;
+                    st.o[nt][d][i + 2] *= c;
+                }
+            }
+    }
+    uint32_t p[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        float e[4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            // A row that has seen nothing yet has references of -inf; its scores are too.
+            const float mu = st.mu[nt][i] == kNegInf ? 0.0f : st.mu[nt][i];
+            const float m = (st.m[nt][i] == kNegInf ? 0.0f : st.m[nt][i]) - ev;
+            st.l[nt][i] += ex2_approx(s[nt][i] - mu) + ex2_approx(s[nt][i + 2] - mu);
+            e[i] = ex2_approx(s[nt][i] - m);
+            e[i + 2] = ex2_approx(s[nt][i + 2] - m);
+        }
+        p[nt][0] = transpose_8x8(pack2h(e[0], e[1]));
+        p[nt][1] = transpose_8x8(pack2h(e[2], e[3]));
+    }
+#pragma unroll
+    for (int w = 0; w < D / 32; ++w) {
+        // Bytes of two keys side by side, two dims per word.
+        const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+        const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+        const uint32_t a[2][4] = {{decode2(x0), decode2(x0 >> 16), decode2(y0), decode2(y0 >> 16)},
+                                  {decode2(x1), decode2(x1 >> 16), decode2(y1), decode2(y1 >> 16)}};
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+                mma_16816(st.o[nt][2 * w + half], a[half][0], a[half][1], a[half][2], a[half][3], p[nt][0], p[nt][1]);
+    }
+}
+
+// The rings while the keys are walked, the warps' results afterwards.
+template <int D, int NT>
+constexpr int kRowsSmem = kWarps * (sizeof(Ring<D>) + kStages * sizeof(Header)) > sizeof(RowsSmem<D, NT>)
+                              ? kWarps * (sizeof(Ring<D>) + kStages * sizeof(Header))
+                              : sizeof(RowsSmem<D, NT>);
+
+template <int D, int NT>
+__global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3) kv_attn_rows(const __grid_constant__ KvAttnArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    RowsSmem<D, NT>& sm = *reinterpret_cast<RowsSmem<D, NT>*>(smem);
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
@@ -126,10 +301,27 @@ __global__ void __launch_bounds__(32 * kWarps) kv_attn_rows(const __grid_constan
     const int least = key_limit(r.len - r.n + t_first, r.len, a.frame);
     const int k0 = split * a.chunk;
     const int k1 = min(most, k0 + a.chunk);
-    if (a.splits > 1 && k0 >= r.len && split > 0) return;  // not read by the join either
+    if (k0 >= r.len && split > 0) return;  // not read by the join either
 
-    uint32_t qf[NT][D / 16][2];
-    int limit[NT][2];
+    const int32_t* table = a.b.table + (int64_t)b * a.b.width;
+    const int bmask = (1 << a.c.block_log2) - 1;
+    constexpr int kStep = kWarps * kGranule;
+    int key = k0 + warp * kGranule;
+    Ring<D>& ring = reinterpret_cast<Ring<D>*>(smem)[warp];
+    Header* hdr = reinterpret_cast<Header*>(smem + kWarps * sizeof(Ring<D>)) + warp * kStages;
+    // Granules load[0 .. kStages - 1) are on their way before the first is computed.
+    int page = key < k1 ? table[key >> a.c.block_log2] : 0;
+    int load = key;
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        const int now = page;
+        if (load + kStep < k1) page = table[(load + kStep) >> a.c.block_log2];
+        if (load < k1) load_granule<D>(ring, hdr, i, a, now, head, load & bmask, lane);
+        cp_async_commit();
+        load += kStep;
+    }
+
+    RowsState<D, NT> st;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int row = r0 + nt * 8 + gid;
@@ -138,133 +330,72 @@ __global__ void __launch_bounds__(32 * kWarps) kv_attn_rows(const __grid_constan
         if (in)
             qp += (int64_t)(r.first + row / a.group) * a.q.token_stride +
                   (int64_t)(head * a.group + row % a.group) * a.q.head_stride + tig * 16;
+        uint32_t top = 0;
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
             uint2 w = make_uint2(0, 0);
             if (in) w = *reinterpret_cast<const uint2*>(qp + (s >> 2) * 64 + (s & 3) * 4);
-            qf[nt][s][0] = w.x;
-            qf[nt][s][1] = w.y;
+            st.q[nt][s][0] = w.x;
+            st.q[nt][s][1] = w.y;
+            top = absmax2(w.x, absmax2(w.y, top));
         }
+        top = fold_halves(top);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // Power of two that brings the row's largest |q| to [2^14, 2^15).
+        const int e = max(-110, min(110, 14 + 127 - (int)(top >> 7)));
+        const float f = __uint_as_float((uint32_t)(127 + e) << 23), back = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t w = st.q[nt][s][i];
+                st.q[nt][s][i] = pack2h(bf16_lo(w) * f, bf16_hi(w) * f);
+            }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+            st.cq[nt][i] = a.scale_log2 * __shfl_sync(0xffffffffu, back, (2 * tig + i) * 4);
             const int lr = r0 + nt * 8 + 2 * tig + i;
-            limit[nt][i] = lr < rows ? key_limit(r.len - r.n + lr / a.group, r.len, a.frame) : 0;
+            st.limit[nt][i] = lr < rows ? key_limit(r.len - r.n + lr / a.group, r.len, a.frame) : 0;
+            st.m[nt][i] = st.mu[nt][i] = kNegInf;
+            st.l[nt][i] = 0.0f;
         }
-    }
-    float m[NT][2], l[NT][2], o[NT][D / 16][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        m[nt][0] = m[nt][1] = kNegInf;
-        l[nt][0] = l[nt][1] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
+        for (int i = 0; i < D / 16; ++i) st.o[nt][i][0] = st.o[nt][i][1] = st.o[nt][i][2] = st.o[nt][i][3] = 0.0f;
     }
 
-    const int32_t* table = a.b.table + (int64_t)b * a.b.width;
-    const int bmask = (1 << a.c.block_log2) - 1;
-    constexpr int kStep = kWarps * kGranule;
-    int key = k0 + warp * kGranule;
-    Granule<D> next;
-    int page = key < k1 ? table[key >> a.c.block_log2] : 0;
-    if (key < k1) load_granule<D>(next, a, page, head, key & bmask, gid, tig);
-    page = key + kStep < k1 ? table[(key + kStep) >> a.c.block_log2] : 0;
+    int stage = 0;
     for (; key < k1; key += kStep) {
-        const Granule<D> g = next;
-        if (key + kStep < k1) load_granule<D>(next, a, page, head, (key + kStep) & bmask, gid, tig);
-        if (key + 2 * kStep < k1) page = table[(key + 2 * kStep) >> a.c.block_log2];
-        if (!g.ok) continue;
-
-        const CodeScale ck = code_scale(g.ks);
-        const bool big_k = ck.rest != kBf16One2;
-        float s[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-            const uint32_t x = g.k[0][i], y = g.k[1][i];
-            uint32_t a0 = mul_bf16x2(spread_codes(x, x, spread_sel(0, 1)), ck.m);
-            uint32_t a1 = mul_bf16x2(spread_codes(y, y, spread_sel(0, 1)), ck.m);
-            uint32_t a2 = mul_bf16x2(spread_codes(x, x, spread_sel(2, 3)), ck.m);
-            uint32_t a3 = mul_bf16x2(spread_codes(y, y, spread_sel(2, 3)), ck.m);
-            if (big_k) {
-                a0 = mul_bf16x2(a0, ck.rest), a1 = mul_bf16x2(a1, ck.rest);
-                a2 = mul_bf16x2(a2, ck.rest), a3 = mul_bf16x2(a3, ck.rest);
-            }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_16816(s[nt], a0, a1, a2, a3, qf[nt][i][0], qf[nt][i][1]);
+        cp_async_wait<kStages - 2>();
+        __syncwarp();  // every lane's pieces of this granule; the one before has been read
+        const int to = stage == 0 ? kStages - 1 : stage - 1;
+        if (load < k1) {
+            const int now = page;
+            if (load + kStep < k1) page = table[(load + kStep) >> a.c.block_log2];
+            load_granule<D>(ring, hdr, to, a, now, head, load & bmask, lane);
         }
-        bool over = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s[nt][i] *= a.scale_log2;
-                if (key + kGranule > least && key + gid + 8 * (i >> 1) >= limit[nt][i & 1]) s[nt][i] = kNegInf;
-                over |= s[nt][i] > m[nt][i & 1] + kLazy;
-            }
-        if (__any_sync(0xffffffffu, over)) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float t = fmaxf(s[nt][i], s[nt][i + 2]);
-                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
-                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
-                    t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                    const float to = fmaxf(m[nt][i], t);
-                    const float c = to == kNegInf ? 1.0f : ex2_approx(m[nt][i] - to);
-                    m[nt][i] = to;
-                    l[nt][i] *= c;
-#pragma unroll
-                    for (int d = 0; d < D / 16; ++d) {
-                        o[nt][d][i] *= c;
-                        o[nt][d][i + 2] *= c;
-                    }
-                }
-        }
-        uint32_t p[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float ref = m[nt][i & 1] == kNegInf ? 0.0f : m[nt][i & 1];
-                s[nt][i] = ex2_approx(s[nt][i] - ref);
-                l[nt][i & 1] += s[nt][i];
-            }
-            p[nt][0] = transpose_8x8(pack2(s[nt][0], s[nt][1]));
-            p[nt][1] = transpose_8x8(pack2(s[nt][2], s[nt][3]));
-        }
-        const CodeScale cs = code_scale(g.vs);
-        const bool big = cs.rest != kBf16One2;
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint32_t e0 = spread_sel(2 * half, 2 * half + 4), e1 = spread_sel(2 * half + 1, 2 * half + 5);
-                uint32_t a0 = mul_bf16x2(spread_codes(g.v[0][w], g.v[1][w], e0), cs.m);
-                uint32_t a1 = mul_bf16x2(spread_codes(g.v[0][w], g.v[1][w], e1), cs.m);
-                uint32_t a2 = mul_bf16x2(spread_codes(g.v[2][w], g.v[3][w], e0), cs.m);
-                uint32_t a3 = mul_bf16x2(spread_codes(g.v[2][w], g.v[3][w], e1), cs.m);
-                if (big) {
-                    a0 = mul_bf16x2(a0, cs.rest), a1 = mul_bf16x2(a1, cs.rest);
-                    a2 = mul_bf16x2(a2, cs.rest), a3 = mul_bf16x2(a3, cs.rest);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma_16816(o[nt][2 * w + half], a0, a1, a2, a3, p[nt][0], p[nt][1]);
-            }
+        cp_async_commit();
+        load += kStep;
+        attend_granule<D, NT>(st, ring.k[stage], ring.v[stage], hdr[stage], key, least, r.len, gid, tig);
+        stage = stage == kStages - 1 ? 0 : stage + 1;
     }
+    cp_async_wait<0>();
+    __syncthreads();  // the rings' memory becomes sm
 
-    // Join the warps: per row the common reference, then the scaled sums.
+    // Join the warps: per row the common references, then the scaled sums.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 4);
-            l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 8);
-            l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], 16);
+            float l = st.l[nt][i];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
             if (gid == 0) {
-                sm.m[warp][nt * 8 + 2 * tig + i] = m[nt][i];
-                sm.l[warp][nt * 8 + 2 * tig + i] = l[nt][i];
+                const int q = nt * 8 + 2 * tig + i;
+                sm.m[warp][q] = st.m[nt][i];
+                sm.mu[warp][q] = st.mu[nt][i];
+                sm.l[warp][q] = l;
             }
         }
     __syncthreads();
@@ -276,11 +407,11 @@ __global__ void __launch_bounds__(32 * kWarps) kv_attn_rows(const __grid_constan
             float top = sm.m[0][q];
 #pragma unroll
             for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm.m[w][q]);
-            const float c = top == kNegInf ? 0.0f : ex2_approx(m[nt][i] - top);
+            const float c = top == kNegInf ? 0.0f : ex2_approx(st.m[nt][i] - top);
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
                 // Row gid of column tile d is dim gid (D / 8) + 2 d, row gid + 8 the next one.
-                float2 x = make_float2(o[nt][d][i] * c, o[nt][d][i + 2] * c);
+                float2 x = make_float2(st.o[nt][d][i] * c, st.o[nt][d][i + 2] * c);
                 *reinterpret_cast<float2*>(&sm.o[warp][q][gid * (D / 8) + 2 * d]) = x;
             }
         }
@@ -290,30 +421,37 @@ __global__ void __launch_bounds__(32 * kWarps) kv_attn_rows(const __grid_constan
         const int q = at / (D / 4), d = (at % (D / 4)) * 4;
         const int row = r0 + q;
         if (row >= rows) break;
-        float top = sm.m[0][q];
+        float top = sm.m[0][q], mu = sm.mu[0][q];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm.m[w][q]);
+        for (int w = 1; w < kWarps; ++w) {
+            top = fmaxf(top, sm.m[w][q]);
+            mu = fmaxf(mu, sm.mu[w][q]);
+        }
         float sum = 0.0f;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            if (top != kNegInf) sum += sm.l[w][q] * ex2_approx(sm.m[w][q] - top);
+            if (mu != kNegInf) sum += sm.l[w][q] * ex2_approx(sm.mu[w][q] - mu);
             const float4 y = *reinterpret_cast<const float4*>(&sm.o[w][q][d]);
             x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
         }
-        const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-        x.x *= inv, x.y *= inv, x.z *= inv, x.w *= inv;
+        // out = x 2^(top - mu) / sum; the power in two steps, it may reach 2^-128.
+        const bool some = sum > 0.0f || sum != sum;
+        const float half = some ? ex2_approx(0.5f * (top - mu)) : 0.0f;
+        const float inv = some ? half / sum : 0.0f;
+        x.x = x.x * half * inv, x.y = x.y * half * inv, x.z = x.z * half * inv, x.w = x.w * half * inv;
         const int64_t token = r.first + row / a.group;
         const int qh = head * a.group + row % a.group;
         const int64_t flat = token * a.q.heads + qh;
+        const float lse = mu == kNegInf ? kNegInf : mu + lg2_approx(sum);
         if (a.splits > 1) {
             const int64_t part = split * total_rows + flat;
             *reinterpret_cast<float4*>(a.part_o + part * D + d) = x;
-            if (d == 0) a.part_lse[part] = top == kNegInf ? kNegInf : top + lg2_approx(sum);
+            if (d == 0) a.part_lse[part] = lse;
         } else {
             *reinterpret_cast<uint2*>(a.out.ptr + token * a.out.token_stride + (int64_t)qh * a.out.head_stride + d) =
                 make_uint2(pack2(x.x, x.y), pack2(x.z, x.w));
-            if (d == 0 && a.lse) a.lse[flat] = top == kNegInf ? kNegInf : 0.6931471805599453f * (top + lg2_approx(sum));
+            if (d == 0 && a.lse) a.lse[flat] = lse * 0.6931471805599453f;
         }
     }
 }
@@ -372,14 +510,14 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
 KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads, int num_sms) {
     KvAttnPlan p{};
     const int64_t rows = (int64_t)b.max_new * (q_heads / c.heads);
-    p.tensor = rows > 16;
-    p.rows_per_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : 256;
+    p.tensor = rows > 32;
+    p.rows_per_tile = rows <= 8 ? 8 : rows <= 32 ? 16 : 256;
     const int64_t tiles = (rows + p.rows_per_tile - 1) / p.rows_per_tile;
     p.row_tiles = (int32_t)(tiles < 1 ? 1 : tiles);
     const int64_t ctas = (int64_t)b.n * p.row_tiles * c.heads;
-    const int64_t fill = p.tensor ? num_sms : 4ll * num_sms;
-    const int64_t least = p.tensor ? 512 : 256;
-    int64_t splits = fill / ctas;
+    const int64_t fill = p.tensor ? num_sms : 16ll * num_sms;
+    const int64_t least = 512;
+    int64_t splits = p.tensor ? fill / ctas : (fill + ctas - 1) / ctas;
     const int64_t most = (b.max_kv + least - 1) / least;
     if (splits > most) splits = most;
     if (splits < 1) splits = 1;
@@ -393,13 +531,26 @@ KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads,
     return p;
 }
 
+template <int D, int NT>
+static cudaError_t launch_rows(dim3 grid, const KvAttnArgs& a, cudaStream_t stream) {
+    static bool attr_done[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !attr_done[dev]) {
+        e = cudaFuncSetAttribute(kv_attn_rows<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRowsSmem<D, NT>);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) attr_done[dev] = true;
+    }
+    return launch_pdl(kv_attn_rows<D, NT>, grid, dim3(32 * kWarps), kRowsSmem<D, NT>, stream, 1, a);
+}
+
 template <int D>
 static cudaError_t launch_for(const KvAttnPlan& p, const KvAttnArgs& a, cudaStream_t stream) {
     const dim3 grid((unsigned)((int64_t)a.b.n * a.row_tiles * a.splits), (unsigned)a.c.heads);
     cudaError_t e = p.tensor ? launch_kv_attn_tiles(a, stream)
-                    : p.rows_per_tile == 8
-                        ? launch_pdl(kv_attn_rows<D, 1>, grid, dim3(32 * kWarps), 0, stream, 1, a)
-                        : launch_pdl(kv_attn_rows<D, 2>, grid, dim3(32 * kWarps), 0, stream, 1, a);
+                    : p.rows_per_tile == 8 ? launch_rows<D, 1>(grid, a, stream)
+                                           : launch_rows<D, 2>(grid, a, stream);
     if (e != cudaSuccess || a.splits == 1) return e;
     const int64_t rows = (int64_t)a.b.max_new * a.q.heads;
     return launch_pdl(kv_attn_join<D>, dim3((unsigned)((rows + 7) / 8), (unsigned)a.b.n), dim3(256), 0, stream, 1, a);
