@@ -1,9 +1,10 @@
 // What the rotary, cache and attention kernels share: their launch arguments,
 // the checks of lengths and block indices that live in device memory, and the
-// E4M3 -> bf16 decoding of cached codes.
+// decoding of cached codes.
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "fp8dit_internal.cuh"
 
@@ -122,43 +123,34 @@ __device__ __forceinline__ float lg2_approx(float x) {
     return y;
 }
 
-// E4M3 codes as bf16 bit patterns: moving a code's sign to bit 15 and its
-// exponent and mantissa to bits 10..4 gives code x 2^-120 exactly, subnormal
-// codes included (bf16's subnormals continue E4M3's), in three instructions
-// for two codes: a byte permute that spreads two bytes to 16-bit lanes with
-// their sign above them, a shift and a mask. The NaN codes come out as +-480,
-// so bytes that nothing has written never turn into a NaN.
-constexpr uint32_t kCodeMask = 0x87f087f0u;
-__device__ __forceinline__ uint32_t spread_codes(uint32_t a, uint32_t b, uint32_t sel) {
+// Two E4M3 codes (the low 16 bits) -> two fp16, exact.
+__device__ __forceinline__ uint32_t decode2(uint32_t codes) {
     uint32_t d;
-    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(sel));
-    return (d << 4) & kCodeMask;
-}
-// Selector of spread_codes: byte i for the low lane and byte j for the high
-// one, 0..3 of a, 4..7 of b (bit 3 of a selector digit repeats the byte's sign).
-__host__ __device__ constexpr uint32_t spread_sel(uint32_t i, uint32_t j) {
-    return i | (i | 8) << 4 | j << 8 | (j | 8) << 12;
-}
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(d) : "r"(codes));
     return d;
 }
-// The factor pair that takes spread codes to code x S, S = 2^n, -120 <= n <=
-// 120: 2^(120 + n) is a bf16 up to n = 7; above, the rest is a second factor
-// (1 otherwise).
-struct CodeScale {
-    uint32_t m;     // 2^(120 + min(n, 7)), twice
-    uint32_t rest;  // 2^max(n - 7, 0), twice
-};
-constexpr uint32_t kBf16One2 = 0x3f803f80u;
-__device__ __forceinline__ CodeScale code_scale(float s) {
-    const int e = (int)((__float_as_uint(s) >> 23) & 0xff);  // n + 127, 7 .. 247
-    const int lo = e < 134 ? e : 134;
-    const uint32_t m = (uint32_t)(lo + 120) << 7;   // biased exponent in a bf16
-    const uint32_t r = (uint32_t)(127 + e - lo) << 7;
-    return CodeScale{m | m << 16, r | r << 16};
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
 }
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// fp16 and the ranges. The attention kernels multiply in fp16: every E4M3 code
+// is exact there and decoding is one instruction for two codes (four to bf16).
+// q is brought to [2^14, 2^15) by a power of two per row (q_exponent, from the
+// row's largest |q|), undone in the score; what lies 2^-38 below the row's
+// largest is lost, as in any fp32 sum of products.
+__device__ __forceinline__ int q_exponent(uint32_t amax_bf16_bits) {
+    return max(-110, min(110, 14 + 127 - (int)(amax_bf16_bits >> 7)));
+}
+__device__ __forceinline__ float pow2f(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }  // -126 .. 127
+// log2 of a block's scale (a power of two).
+__device__ __forceinline__ int scale_log2_of(float s) { return (int)(__float_as_uint(s) >> 23) - 127; }
+
+constexpr float kLog2ToNat = 0.6931471805599453f;
 
 #endif  // __CUDACC__
 

@@ -484,7 +484,7 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
                  : "memory");
 }
 
-// ---- the same for a whole converged warp, of which one lane (lead != 0, see
+// ---- kind::f16 (fp16 or bf16 by the instruction descriptor) for a whole converged warp, of which one lane (lead != 0, see
 // elect_one) issues: the operands then stay in uniform registers. Issued from
 // a one-lane branch every operand of every MMA is moved there first, ~65
 // cycles per MMA, which a chain of 128 x 128 x 16 MMAs (64 cycles) cannot hide.
@@ -497,7 +497,7 @@ __device__ __forceinline__ uint32_t elect_one() {
         : "=r"(r));
     return r;
 }
-__device__ __forceinline__ void mma_bf16_warp(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+__device__ __forceinline__ void mma_f16_warp(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                               uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, l;\n\t"
@@ -508,7 +508,7 @@ __device__ __forceinline__ void mma_bf16_warp(uint32_t lead, uint32_t d_tmem, ui
         : "memory");
 }
 // A from TMEM.
-__device__ __forceinline__ void mma_bf16_tmem_a_warp(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+__device__ __forceinline__ void mma_f16_tmem_a_warp(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
                                                      uint32_t idesc, uint32_t accumulate) {
     asm volatile(
         "{\n\t.reg .pred p, l;\n\t"
@@ -644,6 +644,11 @@ __host__ __device__ constexpr uint32_t umma_idesc_e4m3_f32(int M, int N) {
 // and 10-12), F32 accumulator, both K-major.
 __host__ __device__ constexpr uint32_t umma_idesc_bf16_f32(int M, int N) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// The same with FP16 A and B (format 0).
+__host__ __device__ constexpr uint32_t umma_idesc_f16_f32(int M, int N) {
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
 #endif  // __CUDACC__

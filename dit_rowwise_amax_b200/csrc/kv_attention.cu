@@ -21,15 +21,12 @@
 // 2 tig + 9, whose bytes a permute pairs across keys. P^T comes out of S^T by
 // an 8 x 8 transpose in registers (movmatrix).
 //
-// Why fp16: an E4M3 code is exact in fp16 and one cvt turns two codes into
-// two fp16 (decoding to bf16 takes four instructions, and this kernel is bound
-// by issue slots before HBM if it does: 520 against 300 per granule). Neither
-// range is at risk: q is brought to 2^14 by a power of two per row, undone in
-// the score (its bits below 2^-24 of the row's largest are lost, as in any
-// fp32 sum); K's scale multiplies the score; V's is in the exponent of P, with
-// a reference m of its own, so P is 2^-25 exact relative to the row's largest
+// The products are fp16 (attention.cuh says why; decoding to bf16 this kernel
+// issued 520 instructions per granule instead of 310 and was bound by them).
+// K's scale multiplies the score; V's is in the exponent of P, with a
+// reference m of its own, so P is exact to 2^-25 of the row's largest
 // contribution however V's scales differ. The softmax sum takes a second
-// exponential 2^(s - mu) in fp32.
+// exponential 2^(s - mu), in fp32.
 //
 // Both references are lazy: they only move when a score exceeds them by 8
 // (log2 units), so the usual granule needs one vote and no shuffles; p is at
@@ -40,7 +37,6 @@
 #include "attention.cuh"
 #include "fp8_codec.cuh"
 
-#include <cuda_fp16.h>
 
 namespace fp8dit {
 namespace {
@@ -50,20 +46,6 @@ constexpr int kGranule = 16;
 constexpr float kLazy = 8.0f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack2h(float lo, float hi) {
-    __half2 v = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-// Two E4M3 codes (low 16 bits) -> two fp16, exact.
-__device__ __forceinline__ uint32_t decode2(uint32_t codes) {
-    uint32_t d;
-    asm("{\n\t.reg .b16 c;\n\tcvt.u16.u32 c, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, c;\n\t}" : "=r"(d) : "r"(codes));
-    return d;
-}
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -191,7 +173,7 @@ __device__ __forceinline__ void attend_granule(RowsState<D, NT>& st, const uint8
         }
     }
     // V's scale is a power of two: its log2 is its exponent.
-    const float ev = (float)((int)(__float_as_uint(vs) >> 23) - 127);
+    const float ev = (float)scale_log2_of(vs);
     bool over = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -256,8 +238,8 @@ __device__ __forceinline__ void attend_granule(RowsState<D, NT>& st, const uint8
             e[i] = ex2_approx(s[nt][i] - m);
             e[i + 2] = ex2_approx(s[nt][i + 2] - m);
         }
-        p[nt][0] = transpose_8x8(pack2h(e[0], e[1]));
-        p[nt][1] = transpose_8x8(pack2h(e[2], e[3]));
+        p[nt][0] = transpose_8x8(pack_f16x2(e[0], e[1]));
+        p[nt][1] = transpose_8x8(pack_f16x2(e[2], e[3]));
     }
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
@@ -342,15 +324,14 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3) kv_attn_rows(con
         top = fold_halves(top);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // Power of two that brings the row's largest |q| to [2^14, 2^15).
-        const int e = max(-110, min(110, 14 + 127 - (int)(top >> 7)));
-        const float f = __uint_as_float((uint32_t)(127 + e) << 23), back = __uint_as_float((uint32_t)(127 - e) << 23);
+        const int e = q_exponent(top);
+        const float f = pow2f(e), back = pow2f(-e);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const uint32_t w = st.q[nt][s][i];
-                st.q[nt][s][i] = pack2h(bf16_lo(w) * f, bf16_hi(w) * f);
+                st.q[nt][s][i] = pack_f16x2(bf16_lo(w) * f, bf16_hi(w) * f);
             }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -450,8 +431,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3) kv_attn_rows(con
             if (d == 0) a.part_lse[part] = lse;
         } else {
             *reinterpret_cast<uint2*>(a.out.ptr + token * a.out.token_stride + (int64_t)qh * a.out.head_stride + d) =
-                make_uint2(pack2(x.x, x.y), pack2(x.z, x.w));
-            if (d == 0 && a.lse) a.lse[flat] = lse * 0.6931471805599453f;
+                make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+            if (d == 0 && a.lse) a.lse[flat] = lse * kLog2ToNat;
         }
     }
 }
@@ -497,8 +478,8 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
     const int qh = (int)(row % a.q.heads);
     uint16_t* dst = a.out.ptr + token * a.out.token_stride + (int64_t)qh * a.out.head_stride + lane * V;
 #pragma unroll
-    for (int j = 0; j < V; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack2(x[j] * inv, x[j + 1] * inv);
-    if (lane == 0 && a.lse) a.lse[flat] = top == kNegInf ? kNegInf : 0.6931471805599453f * (top + lg2_approx(sum));
+    for (int j = 0; j < V; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack_bf16x2(x[j] * inv, x[j + 1] * inv);
+    if (lane == 0 && a.lse) a.lse[flat] = top == kNegInf ? kNegInf : kLog2ToNat * (top + lg2_approx(sum));
 }
 
 }  // namespace
@@ -510,8 +491,8 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
 KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads, int num_sms) {
     KvAttnPlan p{};
     const int64_t rows = (int64_t)b.max_new * (q_heads / c.heads);
-    p.tensor = rows > 32;
-    p.rows_per_tile = rows <= 8 ? 8 : rows <= 32 ? 16 : 256;
+    p.tensor = rows > 16;
+    p.rows_per_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : 256;
     const int64_t tiles = (rows + p.rows_per_tile - 1) / p.rows_per_tile;
     p.row_tiles = (int32_t)(tiles < 1 ? 1 : tiles);
     const int64_t ctas = (int64_t)b.n * p.row_tiles * c.heads;

@@ -1,46 +1,53 @@
 // Attention over the E4M3 cache for many query rows: sm_100a tensor cores.
 //
-// One CTA takes up to 256 rows (new tokens x the query heads of one kv head,
-// two tiles of 128), one kv head and one range of keys, and walks the range in
-// tiles of 128 keys:
+// One CTA takes up to 256 rows (new tokens x the query heads of one kv head),
+// one kv head and one range of keys, and walks the range in tiles of 128 keys
+// with two slots, each 128 rows with a score tile S and an output O in TMEM:
 //     S = Q K^T        tcgen05.mma, Q and K in shared memory, S in TMEM
-//     P = 2^(c S - m)  two threads per row: TMEM -> registers -> bf16 -> TMEM
+//     P = 2^(c S - m)  two threads per row: TMEM -> registers -> fp16 -> TMEM
 //     O += P V         tcgen05.mma, P from TMEM, V in shared memory, O in TMEM
-// one pass over the keys, with a running maximum and sum per row. The tensor
-// cores multiply bf16 (q is bf16, and code x S is exact in bf16), so the
-// cached codes are decoded on the way.
+// one pass over the keys, with a running maximum and sum per row. With more
+// than 128 rows the slots are two row tiles that share every key tile; with
+// fewer both slots hold the same rows and take the even and the odd key tiles
+// (dual), and their results are joined at the end. Either way one slot's
+// softmax runs while the tensor cores work for the other.
+//
+// The products are fp16 (attention.cuh says why). K's block scale multiplies
+// the scores; V is decoded as code x 2^(n - r), n its block's scale exponent
+// and r the largest one the CTA has met so far, so O is in units of 2^r and is
+// brought along when r grows. A V block is exact down to 2^-15 of the largest,
+// and better than P's own rounding down to 2^-24.
 //
 // Warp roles (24 warps, one CTA per SM):
-//   0-7, 8-15  softmax of row tile 0 and 1: two threads share a row, 64 keys
-//              each; the warp with the same rows is four warps further on, and
-//              the two exchange their maxima through shared memory. While one
-//              tile's softmax runs, the tensor cores work on the other's.
-//   16-19      decode a raw tile of codes into the 128-byte-swizzled bf16
+//   0-7, 8-15  softmax of slot 0 and 1: two threads share a row, 64 keys each;
+//              the warp with the same rows is four warps further on, and the
+//              two exchange their maxima through shared memory.
+//   16-19      decode 64 keys' codes at a time into the 128-byte-swizzled fp16
 //              layout the MMAs read (K: row = key, K-major; V: the same bytes
 //              read MN-major, so neither is transposed).
-//   20         looks block indices up and bulk-copies the blocks' codes
+//   20         looks block indices and scales up and bulk-copies the codes
 //              (untiled: a block and head is one contiguous piece).
-//   21         issues the MMAs (one thread), owns TMEM.
-// Shared memory at dim 128: Q 64 KB, two decoded K and two V tiles 128 KB, two
-// raw tiles 32 KB. TMEM: S (P over it) 2 x 128 columns, O 2 x dim columns.
+//   21         issues the MMAs (the converged warp, one lane), owns TMEM.
+// Shared memory at dim 128: Q 64 KB, two decoded K and two V tiles 128 KB,
+// four raw stages 32 KB. TMEM: S (P over it) 2 x 128 columns, O 2 x dim.
 //
 // Bound: per 256 x 128 tile at dim 128 the MMAs take 2048 cycles and so do the
-// 32768 exponentials at 16 per cycle; decoding adds about a third of a warp
-// instruction per key byte to the issue slots. Loads are far below HBM.
+// 32768 exponentials at 16 per cycle. Loads are far below HBM.
 //
 // The running maximum is lazy: a row's reference moves, and O is rescaled,
 // only when a score exceeds it by 8 (log2 units), so after the first tiles O
 // stays in TMEM untouched by the softmax threads; p is at most 2^8.
 //
 // Every wait is bounded; an expired one raises the error word and the CTA's
-// abort flag, lets copies and MMAs land, frees TMEM and returns.
+// abort flag, lets copies and MMAs land, frees TMEM and returns. Warps that
+// share a named barrier reach it whatever their waits said.
 #include "attention.cuh"
 #include "fp8_codec.cuh"
 
 namespace fp8dit {
 namespace {
 
-constexpr int kRows = 128;  // rows of a tile = TMEM lanes
+constexpr int kRows = 128;  // rows of a slot = TMEM lanes
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kThreads = 768;
 constexpr float kLazy = 8.0f;
@@ -52,43 +59,45 @@ static_assert(512 * kRegsSoftmax + 128 * kRegsConvert + 128 * kRegsOther <= kThr
 
 // What the roles of a CTA agree on.
 struct Work {
-    int b, head, split, r0, rows;  // first row and rows of the request
-    int k0;                        // first key of the range
-    int n[2], n_max;               // key tiles of each row tile
     Request r;
+    int b, head, split, r0, rows;  // first row; rows of the request
+    int k0;                        // first key of the range
+    int n[2];                      // key tiles of each slot
+    int tiles;                     // key tiles to decode
+    int dual;                      // the slots hold the same rows
 };
+
+constexpr int kRing = 8;  // what the loader tells the softmax per key tile; the two are never 8 tiles apart
 
 struct Bars {
     uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
     uint64_t raw_full[4], raw_empty[4];  // first and second 64 keys of K, of V
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t drain;
+    alignas(16) float k_scale[kRing][kKeys / 16];  // of every 16 keys (read as float4)
+    uint32_t bad[kRing];               // bad blocks, bit per block
+    int v_ref[kRing];                  // exponent r that V is decoded with
+    uint32_t v_mul[2][4];              // 2^(n - r) as fp16, twice: [half of the tile][block]; 0: V counts as 0
     uint32_t tmem;
     int abort;
-    uint32_t bad[8];       // bad blocks of K tile j, bit per block, at j % 8
-    CodeScale scale[4][4]; // [raw stage][block of its 64 keys]
-    int failed[16];        // softmax warp w saw an expired wait
-    Work work;             // kept here, not in every thread's registers
+    int failed[16];  // softmax warp w saw an expired wait
+    Work work;       // kept here, not in every thread's registers
 };
 struct Tops {
-    float v[2][2][kRows];  // [row tile][half of the keys][row]: maxima, at the end sums
+    float v[2][2][kRows];  // [slot][half of the keys][row]: maxima; at the ends |q| and sums
 };
 
 template <int D>
 struct Tile {
-    static constexpr int HALF = kKeys * 128;           // 64 dims of 128 rows: 16 KB
-    static constexpr int BYTES = HALF * (D / 64);      // a bf16 tile of 128 rows
-    static constexpr int RAW = 64 * D;                 // a raw stage: 64 keys' codes
+    static constexpr int HALF = kKeys * 128;       // 64 dims of 128 rows: 16 KB
+    static constexpr int BYTES = HALF * (D / 64);  // an fp16 tile of 128 rows
+    static constexpr int RAW = 64 * D;             // a raw stage: 64 keys' codes
     static constexpr int SMEM = 2 * BYTES + 4 * BYTES + 4 * RAW + (int)sizeof(Tops) + 1024;
     static constexpr uint32_t TMEM_COLS = 512;
     static_assert(sizeof(Bars) <= 1024, "barrier area");
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
 template <int N>
 __device__ __forceinline__ void regs_inc() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -102,56 +111,79 @@ __device__ __forceinline__ f32x2_t f2_add(f32x2_t a, f32x2_t b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // ------------------------------------------------------------ load codes
 template <int D>
-__device__ __forceinline__ void load_role(const KvAttnArgs& a, const Work& w, Bars* sm, uint8_t* raw, int lane) {
+__device__ __forceinline__ void load_role(const KvAttnArgs& a, Bars* sm, uint8_t* raw, int lane) {
+    const Work& w = sm->work;
     const int tlog = a.c.block_log2, T = 1 << tlog, per_tile = kKeys >> tlog;
     const int32_t* table = a.b.table + (int64_t)w.b * a.b.width;
     const int blocks = (w.r.len + T - 1) >> tlog;  // blocks the request has
-    const int rows = min(T, 64);  // rows of a copy: a block, or half of one of 128
-    const uint32_t bytes = (uint32_t)rows * D;
+    const int head = w.head, tiles = w.tiles;
+    const uint32_t bytes = (uint32_t)min(T, 64) * D;  // a copy: a block, or half of one of 128
     volatile int* abort = &sm->abort;
+    // Lane l < per_tile has the tile's block l. Block indices are fetched two
+    // tiles ahead of the copies, scales one.
     int at = (w.k0 >> tlog) + lane;
-    int page = lane < per_tile && at < blocks ? table[at] : 0;
-    int done = 0;  // raw stages filled
-    for (int j = 0; j < w.n_max; ++j) {
+    auto fetch_page = [&]() {
+        const int p = lane < per_tile && at < blocks ? table[at] : -1;
         const bool have = lane < per_tile && at < blocks;
-        const bool ok = have && page >= 0 && page < a.c.n_blocks;
-        const int64_t slot = ok ? (int64_t)page * a.c.heads + w.head : 0;
-        const uint32_t bad = __ballot_sync(0xffffffffu, have && !ok);
-        float s[2] = {0.0f, 0.0f};
-        if (ok) {
-            s[0] = a.c.ks[slot];
-            s[1] = a.c.vs[slot];
-        }
         at += per_tile;
-        page = lane < per_tile && at < blocks ? table[at] : 0;
+        return have ? (p >= 0 && p < a.c.n_blocks ? p : -2) : -1;  // -1: past the end, -2: bad
+    };
+    auto fetch_scale = [&](const float* s, int page) {
+        return page >= 0 ? s[(int64_t)page * a.c.heads + head] : 1.0f;
+    };
+    int page = fetch_page(), next = fetch_page();
+    float sk = fetch_scale(a.c.ks, page), sv = fetch_scale(a.c.vs, page);
+    int v_ref = -120;
+    int done = 0;  // raw stages filled
+    for (int g = 0; g < tiles; ++g) {
+        const int after = fetch_page();
+        const float nk = fetch_scale(a.c.ks, next), nv = fetch_scale(a.c.vs, next);
+        const uint32_t bad = __ballot_sync(0xffffffffu, page == -2);
+        v_ref = max(v_ref, __reduce_max_sync(0xffffffffu, page >= 0 ? scale_log2_of(sv) : -120));
+        const int e = scale_log2_of(sv) - v_ref;
+        uint32_t mul = page < 0 || e < -24 ? 0u : e >= -14 ? (uint32_t)(15 + e) << 10 : 1u << (24 + e);
+        mul |= mul << 16;
+        const float sk16 = __shfl_sync(0xffffffffu, sk, (lane << 4 >> tlog) & 31);
+        const int64_t slot = (int64_t)max(page, 0) * a.c.heads + head;
         bool fail = false;
         for (int st = 0; st < 4; ++st) {  // K's two halves, V's two halves
             const int v = st >> 1, half = st & 1;
             const bool mine = T == 128 ? lane == 0 : lane < per_tile && ((lane << tlog) >> 6) == half;
-            const int count = __popc(__ballot_sync(0xffffffffu, mine && ok));
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sm->raw_empty[st], (uint32_t)(j & 1) ^ 1u, abort, a.err))) {
+            const bool copy = mine && page >= 0;
+            const int count = __popc(__ballot_sync(0xffffffffu, copy));
+            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sm->raw_empty[st], (uint32_t)(g & 1) ^ 1u, abort, a.err))) {
                 fail = true;
                 break;
             }
             const int key = (lane << tlog) & 63;  // first key of this lane's copy in the stage
-            if (mine) sm->scale[st][key >> tlog] = ok ? code_scale(v ? s[1] : s[0]) : CodeScale{0u, kBf16One2};
-            if (lane == 0 && st == 0) {
-                sm->bad[j & 7] = bad;
-                if (bad) atomicOr(a.err.word, kDevErrIndex);
+            if (v && mine) sm->v_mul[half][key >> tlog] = mul;
+            if (st == 0) {
+                if (lane < kKeys / 16) sm->k_scale[g % kRing][lane] = sk16;
+                if (lane == 0) {
+                    sm->bad[g % kRing] = bad;
+                    sm->v_ref[g % kRing] = v_ref;
+                    if (bad) atomicOr(a.err.word, kDevErrIndex);
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(&sm->raw_full[st], (uint32_t)count * bytes);
             __syncwarp();
-            if (mine && ok)
+            if (copy)
                 bulk_load_g2s(raw + st * Tile<D>::RAW + key * D,
                               (v ? a.c.v : a.c.k) + ((slot << tlog) + (T == 128 ? 64 * half : 0)) * D, bytes,
                               &sm->raw_full[st]);
             ++done;
         }
         if (fail) break;
+        page = next, next = after, sk = nk, sv = nv;
     }
     if (*abort) {  // let the copies in flight land
         for (int i = max(0, done - 4); i < done; ++i)
@@ -160,64 +192,73 @@ __device__ __forceinline__ void load_role(const KvAttnArgs& a, const Work& w, Ba
 }
 
 // ---------------------------------------------------------- decode codes
-// 16 codes -> 16 bf16 (two 16-byte pieces of a swizzled row).
-__device__ __forceinline__ void decode16(const uint4& w, const CodeScale& c, uint4& lo, uint4& hi) {
-    uint32_t o[8];
-    const uint32_t in[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        o[2 * i] = mul_bf16x2(spread_codes(in[i], in[i], spread_sel(0, 1)), c.m);
-        o[2 * i + 1] = mul_bf16x2(spread_codes(in[i], in[i], spread_sel(2, 3)), c.m);
-    }
-    if (c.rest != kBf16One2) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = mul_bf16x2(o[i], c.rest);
-    }
-    lo = make_uint4(o[0], o[1], o[2], o[3]);
-    hi = make_uint4(o[4], o[5], o[6], o[7]);
-}
-
 template <int D>
-__device__ __forceinline__ void convert_role(const KvAttnArgs& a, const Work& w, Bars* sm, const uint8_t* raw,
-                                             uint8_t* tiles, int t) {
+__device__ __forceinline__ void convert_role(const KvAttnArgs& a, Bars* sm, const uint8_t* raw, uint8_t* tiles, int t) {
     constexpr int VPR = D / 16;  // 16-byte raw vectors per row
     const int tlog = a.c.block_log2;
     const int lane = t & 31;
+    const int n = sm->work.tiles;
+    const int keys = sm->work.r.len - sm->work.k0;  // keys from the range's start on
     volatile int* abort = &sm->abort;
-    for (int j = 0; j < w.n_max; ++j) {
-        const int buf = j & 1;
-#pragma unroll 1
-        for (int st = 0; st < 4; ++st) {
-            const int v = st >> 1, half = st & 1;
+    for (int g = 0; g < n; ++g) {
+        const int buf = g & 1;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
             uint64_t* full = v ? &sm->v_full[buf] : &sm->k_full[buf];
             uint64_t* empty = v ? &sm->v_empty[buf] : &sm->k_empty[buf];
-            bool ok = mbar_wait_bounded(&sm->raw_full[st], (uint32_t)(j & 1), abort, a.err);
-            if (half == 0) ok = ok && mbar_wait_bounded(empty, (uint32_t)((j >> 1) & 1) ^ 1u, abort, a.err);
-            if (!__all_sync(0xffffffffu, ok)) return;
-            const uint4* src = reinterpret_cast<const uint4*>(raw + st * Tile<D>::RAW);
-            uint8_t* dst = tiles + (2 * v + buf) * Tile<D>::BYTES + half * (64 * 128);
-            uint4 in[VPR / 2];
+#pragma unroll 1
+            for (int half = 0; half < 2; ++half) {
+                const int st = 2 * v + half;
+                bool ok = mbar_wait_bounded(&sm->raw_full[st], (uint32_t)(g & 1), abort, a.err);
+                if (half == 0) ok = ok && mbar_wait_bounded(empty, (uint32_t)((g >> 1) & 1) ^ 1u, abort, a.err);
+                if (!__all_sync(0xffffffffu, ok)) return;
+                const uint4* src = reinterpret_cast<const uint4*>(raw + st * Tile<D>::RAW);
+                uint8_t* dst = tiles + (2 * v + buf) * Tile<D>::BYTES + half * (64 * 128);
+                const int valid = keys - g * kKeys - half * 64;  // rows below it hold tokens
+                uint4 in[VPR / 2];
 #pragma unroll
-            for (int it = 0; it < VPR / 2; ++it) in[it] = src[it * 128 + t];
+                for (int it = 0; it < VPR / 2; ++it) in[it] = src[it * 128 + t];
 #pragma unroll
-            for (int it = 0; it < VPR / 2; ++it) {
-                const int i = it * 128 + t, row = i / VPR, c16 = i % VPR;
-                const CodeScale cs = sm->scale[st][row >> tlog];
-                uint4 lo, hi;
-                decode16(in[it], cs, lo, hi);
-                uint8_t* p = dst + (c16 >> 2) * Tile<D>::HALF + row * 128;
-                const int x = row & 7, c = (c16 & 3) * 2;
-                // Lanes of the two 64-dim halves write their pieces in opposite
-                // order: the eight lanes of a phase then cover all banks.
-                const bool swap = (c16 >> 2) & 1;
-                *reinterpret_cast<uint4*>(p + (((c + (swap ? 1 : 0)) ^ x) << 4)) = swap ? hi : lo;
-                *reinterpret_cast<uint4*>(p + (((c + (swap ? 0 : 1)) ^ x) << 4)) = swap ? lo : hi;
-            }
-            fence_proxy_async_smem();  // before the MMAs (and the next raw copy) touch it
-            __syncwarp();
-            if (lane == 0) {
-                if (half == 1) mbar_arrive(full);
-                mbar_arrive(&sm->raw_empty[st]);
+                for (int it = 0; it < VPR / 2; ++it) {
+                    const int i = it * 128 + t, row = i / VPR, c16 = i % VPR;
+                    uint32_t o[8];
+                    const uint32_t x[4] = {in[it].x, in[it].y, in[it].z, in[it].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        o[2 * k] = decode2(x[k]);
+                        o[2 * k + 1] = decode2(x[k] >> 16);
+                    }
+                    if (v) {
+                        // Rows without a token may hold NaN codes, which a p of 0
+                        // keeps (K's only reach scores that are masked).
+                        uint32_t mul = sm->v_mul[half][row >> tlog];
+                        if (row >= valid) mul = 0;
+                        const __half2 m = *reinterpret_cast<const __half2*>(&mul);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&o[k]), m);
+                            o[k] = *reinterpret_cast<const uint32_t*>(&y);
+                        }
+                        if (mul == 0) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) o[k] = 0;
+                        }
+                    }
+                    uint8_t* p = dst + (c16 >> 2) * Tile<D>::HALF + row * 128;
+                    const int y = row & 7, c = (c16 & 3) * 2;
+                    // Lanes of the two 64-dim halves write their pieces in opposite
+                    // order: the eight lanes of a phase then cover all banks.
+                    const bool swap = (c16 >> 2) & 1;
+                    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+                    *reinterpret_cast<uint4*>(p + (((c + (swap ? 1 : 0)) ^ y) << 4)) = swap ? hi : lo;
+                    *reinterpret_cast<uint4*>(p + (((c + (swap ? 0 : 1)) ^ y) << 4)) = swap ? lo : hi;
+                }
+                fence_proxy_async_smem();  // before the MMAs (and the next raw copy) touch it
+                __syncwarp();
+                if (lane == 0) {
+                    if (half == 1) mbar_arrive(full);
+                    mbar_arrive(&sm->raw_empty[st]);
+                }
             }
         }
     }
@@ -228,14 +269,14 @@ __device__ __forceinline__ void convert_role(const KvAttnArgs& a, const Work& w,
 template <int D>
 __device__ __forceinline__ void mma_role(const KvAttnArgs& a, Bars* sm, const uint8_t* q, const uint8_t* tiles,
                                          uint32_t tmem) {
-    constexpr uint32_t kIdescS = umma_idesc_bf16_f32(128, kKeys);
-    constexpr uint32_t kIdescO = umma_idesc_bf16_f32(128, D) | (1u << 16);  // B (V) is MN-major
+    constexpr uint32_t kIdescS = umma_idesc_f16_f32(128, kKeys);
+    constexpr uint32_t kIdescO = umma_idesc_f16_f32(128, D) | (1u << 16);  // B (V) is MN-major
     volatile int* abort = &sm->abort;
     const uint32_t lead = elect_one();
     // Broadcast from one lane: known to be the same in the whole warp.
     const int n0 = __shfl_sync(0xffffffffu, sm->work.n[0], 0), n1 = __shfl_sync(0xffffffffu, sm->work.n[1], 0);
-    const int n_max = max(n0, n1);
-    const bool two = __shfl_sync(0xffffffffu, sm->work.rows - sm->work.r0, 0) > kRows;
+    const bool dual = __shfl_sync(0xffffffffu, sm->work.dual, 0) != 0;
+    const int rounds = max(n0, n1);
     const uint64_t q_desc = umma_desc_kmajor_sw128(smem_u32(q)), k_desc = umma_desc_kmajor_sw128(smem_u32(tiles));
     const uint64_t v_desc = umma_desc_mnmajor_sw128(smem_u32(tiles) + 2 * Tile<D>::BYTES, Tile<D>::HALF);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -243,56 +284,85 @@ __device__ __forceinline__ void mma_role(const KvAttnArgs& a, Bars* sm, const ui
         tc_fence_after();
         return ok;
     };
-    auto scores = [&](int i, int j) {
-        const uint64_t qd = q_desc + i * (Tile<D>::BYTES >> 4), kd = k_desc + (j & 1) * (Tile<D>::BYTES >> 4);
+    auto k_full = [&](int g) { return wait(&sm->k_full[g & 1], (uint32_t)(g >> 1) & 1u); };
+    auto v_full = [&](int g) { return wait(&sm->v_full[g & 1], (uint32_t)(g >> 1) & 1u); };
+    // S of slot i = Q (row tile qt) K^T (key tile g).
+    auto scores = [&](int i, int qt, int g) {
+        const uint64_t qd = q_desc + qt * (Tile<D>::BYTES >> 4), kd = k_desc + (g & 1) * (Tile<D>::BYTES >> 4);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s) {
             constexpr int kHalf = Tile<D>::HALF >> 4;
             const int off = (s >> 2) * kHalf + (s & 3) * 2;  // in 16-byte units
-            mma_bf16_warp(lead, tmem + i * kKeys, qd + off, kd + off, kIdescS, s > 0);
+            mma_f16_warp(lead, tmem + i * kKeys, qd + off, kd + off, kIdescS, s > 0);
         }
         mma_commit_warp(lead, &sm->s_full[i]);
     };
-    auto output = [&](int i, int j) {
-        const uint64_t vd = v_desc + (j & 1) * (Tile<D>::BYTES >> 4);
+    // O of slot i += P V (key tile g).
+    auto output = [&](int i, int g, bool first) {
+        const uint64_t vd = v_desc + (g & 1) * (Tile<D>::BYTES >> 4);
 #pragma unroll
         for (int s = 0; s < kKeys / 16; ++s)
-            mma_bf16_tmem_a_warp(lead, tmem + 2 * kKeys + i * D, tmem + i * kKeys + s * 8, vd + s * (2048 >> 4), kIdescO,
-                                 j > 0 || s > 0);
+            mma_f16_tmem_a_warp(lead, tmem + 2 * kKeys + i * D, tmem + i * kKeys + s * 8, vd + s * (2048 >> 4), kIdescO,
+                                !first || s > 0);
     };
     bool ok = wait(&sm->q_full[0], 0);
-    if (ok && two) ok = wait(&sm->q_full[1], 0);
-    if (ok && n_max > 0) {
-        ok = wait(&sm->k_full[0], 0);
-        if (ok) {
-            if (n0 > 0) scores(0, 0);
-            if (n1 > 0) scores(1, 0);
+    if (dual) {
+        // Slot i has the tiles 2 j + i, alone; tile g is in buffer g & 1 = i.
+        for (int i = 0; i < 2 && ok; ++i) {
+            if ((i ? n1 : n0) == 0) break;
+            ok = k_full(i);
+            if (!ok) break;
+            scores(i, 0, i);
+            mma_commit_warp(lead, &sm->k_empty[i]);
+        }
+        for (int j = 0; j < rounds && ok; ++j) {
+            for (int i = 0; i < 2 && ok; ++i) {
+                const int n = i ? n1 : n0, g = 2 * j + i;
+                if (j >= n) break;
+                ok = v_full(g) && wait(&sm->p_full[i], (uint32_t)j & 1u);
+                if (!ok) break;
+                output(i, g, j == 0);
+                if (j + 1 == n) mma_commit_warp(lead, &sm->o_full[i]);
+                mma_commit_warp(lead, &sm->v_empty[i]);
+                if (j + 1 < n) {
+                    ok = k_full(g + 2);
+                    if (!ok) break;
+                    scores(i, 0, g + 2);
+                    mma_commit_warp(lead, &sm->k_empty[i]);
+                }
+            }
+        }
+    } else {
+        // Both slots use every key tile; slot 0 may have fewer of them.
+        ok = ok && wait(&sm->q_full[1], 0);
+        if (ok && rounds > 0) ok = k_full(0);
+        if (ok && rounds > 0) {
+            if (n0 > 0) scores(0, 0, 0);
+            scores(1, 1, 0);
             mma_commit_warp(lead, &sm->k_empty[0]);
         }
-    }
-    for (int j = 0; j < n_max && ok; ++j) {
-        const int next = j + 1;
-        ok = wait(&sm->v_full[j & 1], (uint32_t)(j >> 1) & 1u);
-        if (ok && next < n_max) ok = wait(&sm->k_full[next & 1], (uint32_t)(next >> 1) & 1u);
-        if (!ok) break;
-        if (j < n0) {
-            ok = wait(&sm->p_full[0], (uint32_t)j & 1u);
+        for (int j = 0; j < rounds && ok; ++j) {
+            const int next = j + 1;
+            ok = v_full(j);
+            if (ok && next < n1) ok = k_full(next);
             if (!ok) break;
-            output(0, j);
-            if (next == n0) mma_commit_warp(lead, &sm->o_full[0]);
-            if (next < n0) scores(0, next);
-        }
-        if (j < n1) {
+            if (j < n0) {
+                ok = wait(&sm->p_full[0], (uint32_t)j & 1u);
+                if (!ok) break;
+                output(0, j, j == 0);
+                if (next == n0) mma_commit_warp(lead, &sm->o_full[0]);
+                if (next < n0) scores(0, 0, next);
+            }
             ok = wait(&sm->p_full[1], (uint32_t)j & 1u);
             if (!ok) break;
-            output(1, j);
+            output(1, j, j == 0);
             if (next == n1) mma_commit_warp(lead, &sm->o_full[1]);
             mma_commit_warp(lead, &sm->v_empty[j & 1]);
-            if (next < n1) scores(1, next);
-        } else {
-            mma_commit_warp(lead, &sm->v_empty[j & 1]);
+            if (next < n1) {
+                scores(1, 1, next);
+                mma_commit_warp(lead, &sm->k_empty[next & 1]);
+            }
         }
-        if (next < n_max) mma_commit_warp(lead, &sm->k_empty[next & 1]);
     }
     // Every MMA and every arrival on this CTA's barriers lands before it ends.
     mma_commit_warp(lead, &sm->drain);
@@ -300,51 +370,80 @@ __device__ __forceinline__ void mma_role(const KvAttnArgs& a, Bars* sm, const ui
 }
 
 // --------------------------------------------------------------- softmax
-// Thread t of 128 (a row of row tile i), half h of the keys and of dim.
+// Thread t of 128 (a row of slot i), half h of the keys and of dim.
 template <int D>
-__device__ __forceinline__ void softmax_role(const KvAttnArgs& a, const Work& w, Bars* sm, Tops* tops, uint8_t* q,
+__device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, Tops* tops, uint8_t* q, uint8_t* tiles,
                                              uint32_t tmem, int i, int h, int t) {
+    const Work& w = sm->work;
     const int lane = t & 31, warp = 8 * i + 4 * h + (t >> 5), partner = warp ^ 4;
     const uint32_t pair = 1u + 4 * i + (t >> 5);  // named barrier of the two warps that share rows
-    const int row = w.r0 + i * kRows + t;
+    const bool dual = w.dual != 0;
+    const int row = w.r0 + (dual ? 0 : i * kRows) + t;
     const bool in = row < w.rows;
     // Rows past the last one compute on zeros and are not written.
-    const int limit = in ? key_limit(w.r.len - w.r.n + row / a.group, w.r.len, a.frame) : INT32_MAX;
+    const int limit = (in ? key_limit(w.r.len - w.r.n + row / a.group, w.r.len, a.frame) : w.r.len) - w.k0 - 64 * h;
     volatile int* abort = &sm->abort;
+    float c;  // softmax scale * log2(e) / q's scale
     {
         const int token = in ? row / a.group : 0, qh = w.head * a.group + (in ? row % a.group : 0);
         const uint16_t* src = a.q.ptr + (int64_t)(w.r.first + token) * a.q.token_stride + (int64_t)qh * a.q.head_stride;
-        uint8_t* dst = q + i * Tile<D>::BYTES + t * 128;
+        uint4 v[D / 16];
+        uint32_t top = 0;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-            const int c = h * (D / 16) + k;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (in) v = *reinterpret_cast<const uint4*>(src + c * 8);
-            *reinterpret_cast<uint4*>(dst + (c >> 3) * Tile<D>::HALF + (((c & 7) ^ (t & 7)) << 4)) = v;
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (in) v[k] = *reinterpret_cast<const uint4*>(src + (h * (D / 16) + k) * 8);
+            top = absmax8(v[k], top);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->q_full[i]);
+        top = fold_halves(top);
+        tops->v[i][h][t] = __uint_as_float(top);
+        named_barrier_sync(pair, 64);
+        top = max(top, __float_as_uint(*(volatile float*)&tops->v[i][h ^ 1][t]));
+        const int e = q_exponent(top);
+        const float f = pow2f(e);
+        c = a.scale_log2 * pow2f(-e);
+        if (!dual || i == 0) {
+            uint8_t* dst = q + i * Tile<D>::BYTES + t * 128;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                const int p = h * (D / 16) + k;
+                uint32_t* y = &v[k].x;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) y[z] = pack_f16x2(bf16_lo(y[z]) * f, bf16_hi(y[z]) * f);
+                *reinterpret_cast<uint4*>(dst + (p >> 3) * Tile<D>::HALF + (((p & 7) ^ (t & 7)) << 4)) = v[k];
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm->q_full[i]);
+        }
+        named_barrier_sync(pair, 64);  // tops may be written again
     }
     const uint32_t lanes = (uint32_t)(t >> 5) << 21;  // this warp's TMEM lanes: (t / 32) * 32 << 16
     const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + 2 * kKeys + i * D + h * (D / 2);
-    const float c = a.scale_log2;
+    const int n = w.n[i];
     float m = kNegInf, l = 0.0f;
+    int v_ref = -120;  // O is in units of 2^v_ref
     bool ok = true;
-    for (int j = 0; j < w.n[i]; ++j) {
+    for (int j = 0; j < n; ++j) {
+        const int g = dual ? 2 * j + i : j;
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm->s_full[i], (uint32_t)j & 1u, abort, a.err));
         uint32_t s[2][32];
-        float tile_top = kNegInf;
+        float f[4], tile_top = kNegInf;  // f: score factors of 16 keys each
         if (ok) {
             tc_fence_after();
             tmem_ld_32x32b_x32(s_addr + 64 * h, s[0]);
             tmem_ld_32x32b_x32(s_addr + 64 * h + 32, s[1]);
+            const float4 ks = *reinterpret_cast<const float4*>(&sm->k_scale[g % kRing][4 * h]);
+            // Not 0: a masked score of -inf stays one.
+            f[0] = fmaxf(c * ks.x, 0x1p-126f), f[1] = fmaxf(c * ks.y, 0x1p-126f);
+            f[2] = fmaxf(c * ks.z, 0x1p-126f), f[3] = fmaxf(c * ks.w, 0x1p-126f);
+            const int seen = limit - g * kKeys;  // this row sees columns below it
+            const uint32_t bad = *(volatile uint32_t*)&sm->bad[g % kRing];
+            const bool mask = __any_sync(0xffffffffu, seen < 64) || bad;
             tmem_wait_ld();
             tmem_tie32(s[0]);
             tmem_tie32(s[1]);
-            const int seen = limit - (w.k0 + j * kKeys) - 64 * h;  // this row sees columns below it
-            const uint32_t bad = *(volatile uint32_t*)&sm->bad[j & 7];
-            if (__any_sync(0xffffffffu, seen < 64) || bad) {
+            if (mask) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -352,32 +451,40 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, const Work& w,
                         if (32 * k + x >= seen || (bad >> ((64 * h + 32 * k + x) >> a.c.block_log2) & 1u))
                             s[k][x] = __float_as_uint(kNegInf);
             }
-            float top[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
+            float top[4];
 #pragma unroll
-            for (int x = 0; x < 32; x += 2)
+            for (int z = 0; z < 4; ++z) {
+                const uint32_t* y = &s[z >> 1][(z & 1) * 16];
+                float u0 = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
+                float u1 = max3(__uint_as_float(y[3]), __uint_as_float(y[4]), __uint_as_float(y[5]));
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    top[2 * k] = fmaxf(top[2 * k], __uint_as_float(s[k][x]));
-                    top[2 * k + 1] = fmaxf(top[2 * k + 1], __uint_as_float(s[k][x + 1]));
+                for (int x = 6; x < 14; x += 4) {
+                    u0 = max3(u0, __uint_as_float(y[x]), __uint_as_float(y[x + 1]));
+                    u1 = max3(u1, __uint_as_float(y[x + 2]), __uint_as_float(y[x + 3]));
                 }
-            tile_top = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                u0 = max3(u0, __uint_as_float(y[14]), __uint_as_float(y[15]));
+                top[z] = fmaxf(u0, u1) * f[z];
+            }
+            tile_top = fmaxf(max3(top[0], top[1], top[2]), top[3]);
             tops->v[i][h][t] = tile_top;
         } else if (lane == 0) {
             *(volatile int*)&sm->failed[warp] = 1;
         }
-        // Both warps have read their scores (P will overwrite them) and come
-        // here whatever their waits said, so neither is left alone.
+        // Both warps have read their scores (P will overwrite them).
         named_barrier_sync(pair, 64);
         if (!ok || *(volatile int*)&sm->failed[partner]) {
             ok = false;
             break;
         }
         tile_top = fmaxf(tile_top, *(volatile float*)&tops->v[i][h ^ 1][t]);
-        if (__any_sync(0xffffffffu, (tile_top - m) * c > kLazy)) {
+        const int r = *(volatile int*)&sm->v_ref[g % kRing];
+        if (__any_sync(0xffffffffu, tile_top > m + kLazy) || r != v_ref) {
             const float to = fmaxf(m, tile_top);
-            const float f = to == kNegInf ? 1.0f : ex2_approx((m - to) * c);
+            const float down = to == kNegInf ? 1.0f : ex2_approx(m - to);
+            const float fo = down * ex2_approx((float)(v_ref - r));
             m = to;
-            l *= f;
+            l *= down;
+            v_ref = r;
             if (j > 0) {  // O of the earlier tiles is complete: S came after it
 #pragma unroll
                 for (int k = 0; k < D / 32; ++k) {
@@ -385,24 +492,25 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, const Work& w,
                     tmem_ld_32x32b_x16(o_addr + 16 * k, o);
                     tmem_wait_ld16(o);
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                    for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fo);
                     tmem_st_32x32b_x16(o_addr + 16 * k, o);
                 }
             }
         }
-        const float mc = m == kNegInf ? 0.0f : -m * c;
-        const f32x2_t c2 = f2_pack(c, c), mc2 = f2_pack(mc, mc);
+        const float neg = m == kNegInf ? 0.0f : -m;
+        const f32x2_t neg2 = f2_pack(neg, neg);
         f32x2_t sum[2] = {f2_pack(l, 0.0f), f2_pack(0.0f, 0.0f)};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             uint32_t p[16];
 #pragma unroll
             for (int x = 0; x < 16; ++x) {
-                const float2 e =
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(s[k][2 * x]), __uint_as_float(s[k][2 * x + 1])), c2, mc2));
+                const float fx = f[2 * k + (x >> 3)];
+                const float2 e = f2_unpack(f2_fma(
+                    f2_pack(__uint_as_float(s[k][2 * x]), __uint_as_float(s[k][2 * x + 1])), f2_pack(fx, fx), neg2));
                 const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
                 sum[x & 1] = f2_add(sum[x & 1], f2_pack(p0, p1));
-                p[x] = pack2(p0, p1);
+                p[x] = pack_f16x2(p0, p1);
             }
             tmem_st_32x32b_x16(s_addr + 32 * h + 16 * k, p);
         }
@@ -413,58 +521,107 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, const Work& w,
         const float2 t2 = f2_unpack(f2_add(sum[0], sum[1]));
         l = t2.x + t2.y;
     }
-    if (w.n[i] > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm->o_full[i], 0, abort, a.err));
-    // The row's sum over both halves (the last maxima have been read).
-    if (ok)
-        tops->v[i][h][t] = l;
-    else if (lane == 0)
-        *(volatile int*)&sm->failed[warp] = 1;
-    named_barrier_sync(pair, 64);
-    if (!ok || *(volatile int*)&sm->failed[partner]) return;
-    l += *(volatile float*)&tops->v[i][h ^ 1][t];
+    if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm->o_full[i], 0, abort, a.err));
     tc_fence_after();
-    const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+    // The row's sum over both halves.
+    if (ok) tops->v[i][h][t] = l;
+    if (!ok && lane == 0) *(volatile int*)&sm->failed[warp] = 1;
+    named_barrier_sync(pair, 64);
+    if (*(volatile int*)&sm->failed[partner]) ok = false;
+    if (ok) l += *(volatile float*)&tops->v[i][h ^ 1][t];
+
+    // Dual: slot 1 leaves its results in the buffers that only it has used (K's
+    // and V's second; [4 dims][row] float4), slot 0 joins them.
+    float4* other = reinterpret_cast<float4*>(tiles + (h ? 3 : 1) * Tile<D>::BYTES);
+    float* meta = reinterpret_cast<float*>(q + Tile<D>::BYTES) + 3 * kRows * h;  // reference, sum, unit
+    if (dual) {
+        if (i == 1) {
+            if (ok) {
+                meta[t] = m;
+                meta[kRows + t] = l;
+                meta[2 * kRows + t] = (float)v_ref;
+                if (n > 0) {
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        uint32_t o[16];
+                        tmem_ld_32x32b_x16(o_addr + 16 * k, o);
+                        tmem_wait_ld16(o);
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            other[(4 * k + x) * kRows + t] =
+                                make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                            __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+                    }
+                }
+            }
+            if (!ok && lane == 0) *(volatile int*)&sm->failed[warp] = 1;
+        }
+        named_barrier_sync(9, 512);
+        if (i == 1) return;
+        if (*(volatile int*)&sm->failed[warp + 8] || *(volatile int*)&sm->failed[partner + 8]) ok = false;
+    }
+    if (!ok) return;
+    // out = (O x own + O' x theirs), O' of the other slot.
+    float own = 1.0f, theirs = 0.0f;
+    if (dual && w.n[1] > 0) {
+        const float mo = meta[t], to = fmaxf(m, mo);
+        if (to != kNegInf) {
+            const float x = ex2_approx(m - to), y = ex2_approx(mo - to);
+            l = l * x + meta[kRows + t] * y;
+            own = x, theirs = y * ex2_approx(meta[2 * kRows + t] - (float)v_ref);
+        }
+        m = to;
+    }
+    const float inv = l > 0.0f || l != l ? 1.0f / l * pow2f(v_ref) : 0.0f;
+    own *= inv, theirs *= inv;
     // Taken again rather than kept in registers through the loop.
     const int token = in ? row / a.group : 0, qh = w.head * a.group + (in ? row % a.group : 0);
     const int64_t tok = w.r.first + token;
     const int64_t flat = tok * a.q.heads + qh;
     const int64_t part = (int64_t)w.split * a.b.total * a.q.heads + flat;
     if (in && h == 0) {
-        const float lse = m == kNegInf ? kNegInf : m * c + lg2_approx(l);
+        const float lse = m == kNegInf ? kNegInf : m + lg2_approx(l);
         if (a.splits > 1)
             a.part_lse[part] = lse;
         else if (a.lse)
-            a.lse[flat] = lse * 0.6931471805599453f;
+            a.lse[flat] = lse * kLog2ToNat;
     }
 #pragma unroll
-    for (int k = 0; k < D / 64; ++k) {
-        uint32_t o[32];
-        if (w.n[i] > 0) {
-            tmem_ld_32x32b_x32(o_addr + 32 * k, o);
-            tmem_wait_ld();
-            tmem_tie32(o);
+    for (int k = 0; k < D / 32; ++k) {
+        uint32_t o[16];
+        if (n > 0) {
+            tmem_ld_32x32b_x16(o_addr + 16 * k, o);
+            tmem_wait_ld16(o);
         } else {
 #pragma unroll
-            for (int x = 0; x < 32; ++x) o[x] = 0;
+            for (int x = 0; x < 16; ++x) o[x] = 0;
+        }
+        float y[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) y[x] = __uint_as_float(o[x]) * own;
+        if (theirs != 0.0f) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float4 z = other[(4 * k + x) * kRows + t];
+                y[4 * x] = fmaf(z.x, theirs, y[4 * x]);
+                y[4 * x + 1] = fmaf(z.y, theirs, y[4 * x + 1]);
+                y[4 * x + 2] = fmaf(z.z, theirs, y[4 * x + 2]);
+                y[4 * x + 3] = fmaf(z.w, theirs, y[4 * x + 3]);
+            }
         }
         if (!in) continue;
-        const int d = h * (D / 2) + 32 * k;
+        const int d = h * (D / 2) + 16 * k;
         if (a.splits > 1) {
             float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + d);
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-                dst[x] = make_float4(__uint_as_float(o[4 * x]) * inv, __uint_as_float(o[4 * x + 1]) * inv,
-                                     __uint_as_float(o[4 * x + 2]) * inv, __uint_as_float(o[4 * x + 3]) * inv);
+            for (int x = 0; x < 4; ++x) dst[x] = make_float4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
         } else {
-            uint4* dst = reinterpret_cast<uint4*>(a.out.ptr + tok * a.out.token_stride + (int64_t)qh * a.out.head_stride + d);
+            uint4* dst =
+                reinterpret_cast<uint4*>(a.out.ptr + tok * a.out.token_stride + (int64_t)qh * a.out.head_stride + d);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                uint32_t y[4];
-#pragma unroll
-                for (int z = 0; z < 4; ++z)
-                    y[z] = pack2(__uint_as_float(o[8 * x + 2 * z]) * inv, __uint_as_float(o[8 * x + 2 * z + 1]) * inv);
-                dst[x] = make_uint4(y[0], y[1], y[2], y[3]);
-            }
+            for (int x = 0; x < 2; ++x)
+                dst[x] = make_uint4(pack_bf16x2(y[8 * x], y[8 * x + 1]), pack_bf16x2(y[8 * x + 2], y[8 * x + 3]),
+                                    pack_bf16x2(y[8 * x + 4], y[8 * x + 5]), pack_bf16x2(y[8 * x + 6], y[8 * x + 7]));
         }
     }
 }
@@ -474,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles(const __grid_consta
     // Dynamic shared memory starts on a 1024-byte boundary (there is no static
     // one); the swizzled tiles rely on it, so it is checked.
     extern __shared__ __align__(1024) uint8_t q[];
-    uint8_t* tiles = q + 2 * Tile<D>::BYTES;  // K stages 0, 1, V stages 0, 1
+    uint8_t* tiles = q + 2 * Tile<D>::BYTES;  // K buffers 0, 1, V buffers 0, 1
     uint8_t* raw = tiles + 4 * Tile<D>::BYTES;
     Tops* tops = reinterpret_cast<Tops*>(raw + 4 * Tile<D>::RAW);
     Bars* sm = reinterpret_cast<Bars*>(tops + 1);
@@ -501,15 +658,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles(const __grid_consta
     w.r0 = tile * 2 * kRows;
     w.k0 = w.split * a.chunk;
     if (w.r0 >= w.rows || (w.split > 0 && w.k0 >= w.r.len)) return;
-    w.n_max = 0;
+    w.dual = w.rows - w.r0 <= kRows;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int last = min(w.r0 + (i + 1) * kRows, w.rows) - 1;
-        int keys = 0;
-        if (w.r0 + i * kRows < w.rows)
-            keys = min(key_limit(w.r.len - w.r.n + last / a.group, w.r.len, a.frame), w.k0 + a.chunk) - w.k0;
+        const int last = min(w.r0 + (w.dual ? 1 : i + 1) * kRows, w.rows) - 1;
+        const int keys = min(key_limit(w.r.len - w.r.n + last / a.group, w.r.len, a.frame), w.k0 + a.chunk) - w.k0;
         w.n[i] = keys > 0 ? (keys + kKeys - 1) / kKeys : 0;
-        w.n_max = max(w.n_max, w.n[i]);
+    }
+    w.tiles = w.n[1];
+    if (w.dual) {
+        w.n[0] = (w.tiles + 1) / 2;
+        w.n[1] = w.tiles / 2;
     }
 
     if (threadIdx.x == 0) {
@@ -544,16 +703,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles(const __grid_consta
 
     if (warp < 16) {
         regs_inc<kRegsSoftmax>();
-        const int i = warp >> 3;
-        if (sm->work.r0 + i * kRows < sm->work.rows)
-            softmax_role<D>(a, sm->work, sm, tops, q, tmem, i, (warp >> 2) & 1, threadIdx.x & 127);
+        softmax_role<D>(a, sm, tops, q, tiles, tmem, warp >> 3, (warp >> 2) & 1, threadIdx.x & 127);
     } else if (warp < 20) {
         regs_inc<kRegsConvert>();
-        convert_role<D>(a, sm->work, sm, raw, tiles, threadIdx.x & 127);
+        convert_role<D>(a, sm, raw, tiles, threadIdx.x & 127);
     } else {
         regs_dec<kRegsOther>();
         if (warp == 20)
-            load_role<D>(a, sm->work, sm, raw, lane);
+            load_role<D>(a, sm, raw, lane);
         else if (warp == 21)
             mma_role<D>(a, sm, q, tiles, tmem);
     }

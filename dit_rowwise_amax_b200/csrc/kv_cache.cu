@@ -26,7 +26,6 @@ __device__ __forceinline__ int scale_exponent(uint32_t amax_bits) {
     const int n = (int)(amax_bits >> 7) - 127 - 8 + ((amax_bits & 0x7fu) > 0x60u ? 1 : 0);
     return n < -120 ? -120 : n > 120 ? 120 : n;  // exponent field 0 (zero, subnormals) ends at -120
 }
-__device__ __forceinline__ float pow2(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }
 
 __device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -84,11 +83,11 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const __grid_constant__ 
     const int need = scale_exponent(m);
     int n = need;
     if (held) {
-        const int n_old = (int)(__float_as_uint(old) >> 23) - 127;
+        const int n_old = scale_log2_of(old);
         n = max(need, min(max(n_old, -120), 120));
         if (n != n_old) {
             // ratio = 2^(n_old - n): below 2^-126 every code becomes a zero anyway.
-            const float ratio = n_old - n < -126 ? 0.0f : pow2(n_old - n);
+            const float ratio = n_old - n < -126 ? 0.0f : pow2f(n_old - n);
             for (int at = threadIdx.x; at < T * VPR; at += blockDim.x) {
                 if (at >= lo * VPR && at < hi * VPR) continue;  // the new rows
                 uint2* p = reinterpret_cast<uint2*>(codes) + at;
@@ -105,7 +104,7 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const __grid_constant__ 
             }
         }
     }
-    const float inv = pow2(-n);
+    const float inv = pow2f(-n);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         const int at = i * blockDim.x + threadIdx.x, row = at / VPR;
@@ -115,7 +114,7 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const __grid_constant__ 
         o.y = quant4(bf16_lo(v[i].z) * inv, bf16_hi(v[i].z) * inv, bf16_lo(v[i].w) * inv, bf16_hi(v[i].w) * inv);
         reinterpret_cast<uint2*>(codes)[at] = o;
     }
-    if (threadIdx.x == 0) *scale = pow2(n);
+    if (threadIdx.x == 0) *scale = pow2f(n);
 }
 
 }  // namespace

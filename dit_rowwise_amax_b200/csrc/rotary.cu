@@ -22,11 +22,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<uint32_t*>(&v);
-}
-
 template <bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
     __shared__ double turns[FP8DIT_ROTARY_MAX_DIM / 2];
@@ -82,7 +77,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float x = bf16_lo(w[j]), y = bf16_hi(w[j]);
-                    w[j] = pack2(fmaf(x, c[j], -(y * s[j])), fmaf(x, s[j], y * c[j]));
+                    w[j] = pack_bf16x2(fmaf(x, c[j], -(y * s[j])), fmaf(x, s[j], y * c[j]));
                 }
             }
             *reinterpret_cast<uint4*>(dst) = v;
@@ -95,8 +90,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
             for (int j = 0; j < 2; ++j) {
                 const float x0 = bf16_lo(xw[j]), x1 = bf16_hi(xw[j]), y0 = bf16_lo(yw[j]), y1 = bf16_hi(yw[j]);
                 const float c0 = c[2 * j], c1 = c[2 * j + 1], s0 = s[2 * j], s1 = s[2 * j + 1];
-                xw[j] = pack2(fmaf(x0, c0, -(y0 * s0)), fmaf(x1, c1, -(y1 * s1)));
-                yw[j] = pack2(fmaf(x0, s0, y0 * c0), fmaf(x1, s1, y1 * c1));
+                xw[j] = pack_bf16x2(fmaf(x0, c0, -(y0 * s0)), fmaf(x1, c1, -(y1 * s1)));
+                yw[j] = pack_bf16x2(fmaf(x0, s0, y0 * c0), fmaf(x1, s1, y1 * c1));
             }
             *reinterpret_cast<uint2*>(dst) = x2;
             *reinterpret_cast<uint2*>(dst + a.pairs) = y2;
