@@ -4,7 +4,7 @@
 // one kv head and one range of keys, and walks the range in tiles of 128 keys
 // with two slots, each 128 rows with a score tile S and an output O in TMEM:
 //     S = Q K^T        tcgen05.mma, Q and K in shared memory, S in TMEM
-//     P = 2^(c S - m)  two threads per row: TMEM -> registers -> fp16 -> TMEM
+//     P = 2^(c S - m)  a thread per row: TMEM -> registers -> fp16 -> TMEM
 //     O += P V         tcgen05.mma, P from TMEM, V in shared memory, O in TMEM
 // one pass over the keys, with a running maximum and sum per row. With more
 // than 128 rows the slots are two row tiles that share every key tile; with
@@ -18,16 +18,16 @@
 // brought along when r grows. A V block is exact down to 2^-15 of the largest,
 // and better than P's own rounding down to 2^-24.
 //
-// Warp roles (24 warps, one CTA per SM):
-//   0-7, 8-15  softmax of slot 0 and 1: two threads share a row, 64 keys each;
-//              the warp with the same rows is four warps further on, and the
-//              two exchange their maxima through shared memory.
-//   16-19      decode 64 keys' codes at a time into the 128-byte-swizzled fp16
+// Warp roles (20 warps, one CTA per SM):
+//   0-3, 4-7   softmax of slot 0 and 1, a thread per row. P is handed over in
+//              two halves, so the first half's product runs under the second
+//              half's exponentials.
+//   8-15       decode 64 keys' codes at a time into the 128-byte-swizzled fp16
 //              layout the MMAs read (K: row = key, K-major; V: the same bytes
 //              read MN-major, so neither is transposed).
-//   20         looks block indices and scales up and bulk-copies the codes
+//   16         looks block indices and scales up and bulk-copies the codes
 //              (untiled: a block and head is one contiguous piece).
-//   21         issues the MMAs (the converged warp, one lane), owns TMEM.
+//   17         issues the MMAs (the converged warp, one lane), owns TMEM.
 // Shared memory at dim 128: Q 64 KB, two decoded K and two V tiles 128 KB,
 // four raw stages 32 KB. TMEM: S (P over it) 2 x 128 columns, O 2 x dim.
 //
@@ -49,13 +49,13 @@ namespace {
 
 constexpr int kRows = 128;  // rows of a slot = TMEM lanes
 constexpr int kKeys = 128;  // keys of a tile
-constexpr int kThreads = 768;
+constexpr int kThreads = 640;
 constexpr float kLazy = 8.0f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
-// Registers per thread by role, out of the launch's 768 x 80.
-constexpr int kRegsSoftmax = 88, kRegsConvert = 88, kRegsOther = 40;
-static_assert(512 * kRegsSoftmax + 128 * kRegsConvert + 128 * kRegsOther <= kThreads * 80, "register split");
+// Registers per thread by role, out of the launch's 640 x 96.
+constexpr int kRegsSoftmax = 168, kRegsConvert = 56, kRegsOther = 32;
+static_assert(256 * kRegsSoftmax + 256 * kRegsConvert + 128 * kRegsOther <= kThreads * 96, "register split");
 
 // What the roles of a CTA agree on.
 struct Work {
@@ -70,7 +70,7 @@ struct Work {
 constexpr int kRing = 8;  // what the loader tells the softmax per key tile; the two are never 8 tiles apart
 
 struct Bars {
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2];  // p_full: [slot][half of the keys]
     uint64_t raw_full[4], raw_empty[4];  // first and second 64 keys of K, of V
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t drain;
@@ -80,19 +80,15 @@ struct Bars {
     uint32_t v_mul[2][4];              // 2^(n - r) as fp16, twice: [half of the tile][block]; 0: V counts as 0
     uint32_t tmem;
     int abort;
-    int failed[16];  // softmax warp w saw an expired wait
+    int failed[8];  // softmax warp w saw an expired wait
     Work work;       // kept here, not in every thread's registers
 };
-struct Tops {
-    float v[2][2][kRows];  // [slot][half of the keys][row]: maxima; at the ends |q| and sums
-};
-
 template <int D>
 struct Tile {
     static constexpr int HALF = kKeys * 128;       // 64 dims of 128 rows: 16 KB
     static constexpr int BYTES = HALF * (D / 64);  // an fp16 tile of 128 rows
     static constexpr int RAW = 64 * D;             // a raw stage: 64 keys' codes
-    static constexpr int SMEM = 2 * BYTES + 4 * BYTES + 4 * RAW + (int)sizeof(Tops) + 1024;
+    static constexpr int SMEM = 2 * BYTES + 4 * BYTES + 4 * RAW + 1024;
     static constexpr uint32_t TMEM_COLS = 512;
     static_assert(sizeof(Bars) <= 1024, "barrier area");
     static_assert(SMEM <= 232448, "shared memory budget");
@@ -215,12 +211,12 @@ __device__ __forceinline__ void convert_role(const KvAttnArgs& a, Bars* sm, cons
                 const uint4* src = reinterpret_cast<const uint4*>(raw + st * Tile<D>::RAW);
                 uint8_t* dst = tiles + (2 * v + buf) * Tile<D>::BYTES + half * (64 * 128);
                 const int valid = keys - g * kKeys - half * 64;  // rows below it hold tokens
-                uint4 in[VPR / 2];
+                uint4 in[VPR / 4];
 #pragma unroll
-                for (int it = 0; it < VPR / 2; ++it) in[it] = src[it * 128 + t];
+                for (int it = 0; it < VPR / 4; ++it) in[it] = src[it * 256 + t];
 #pragma unroll
-                for (int it = 0; it < VPR / 2; ++it) {
-                    const int i = it * 128 + t, row = i / VPR, c16 = i % VPR;
+                for (int it = 0; it < VPR / 4; ++it) {
+                    const int i = it * 256 + t, row = i / VPR, c16 = i % VPR;
                     uint32_t o[8];
                     const uint32_t x[4] = {in[it].x, in[it].y, in[it].z, in[it].w};
 #pragma unroll
@@ -297,13 +293,18 @@ __device__ __forceinline__ void mma_role(const KvAttnArgs& a, Bars* sm, const ui
         }
         mma_commit_warp(lead, &sm->s_full[i]);
     };
-    // O of slot i += P V (key tile g).
-    auto output = [&](int i, int g, bool first) {
+    // O of slot i += P V (key tile g, the slot's tile j), as P's halves come.
+    auto output = [&](int i, int j, int g) {
         const uint64_t vd = v_desc + (g & 1) * (Tile<D>::BYTES >> 4);
 #pragma unroll
-        for (int s = 0; s < kKeys / 16; ++s)
-            mma_f16_tmem_a_warp(lead, tmem + 2 * kKeys + i * D, tmem + i * kKeys + s * 8, vd + s * (2048 >> 4), kIdescO,
-                                !first || s > 0);
+        for (int half = 0; half < 2; ++half) {
+            if (!wait(&sm->p_full[i][half], (uint32_t)j & 1u)) return false;
+#pragma unroll
+            for (int s = 4 * half; s < 4 * half + 4; ++s)
+                mma_f16_tmem_a_warp(lead, tmem + 2 * kKeys + i * D, tmem + i * kKeys + s * 8, vd + s * (2048 >> 4),
+                                    kIdescO, j > 0 || s > 0);
+        }
+        return true;
     };
     bool ok = wait(&sm->q_full[0], 0);
     if (dual) {
@@ -319,9 +320,8 @@ __device__ __forceinline__ void mma_role(const KvAttnArgs& a, Bars* sm, const ui
             for (int i = 0; i < 2 && ok; ++i) {
                 const int n = i ? n1 : n0, g = 2 * j + i;
                 if (j >= n) break;
-                ok = v_full(g) && wait(&sm->p_full[i], (uint32_t)j & 1u);
+                ok = v_full(g) && output(i, j, g);
                 if (!ok) break;
-                output(i, g, j == 0);
                 if (j + 1 == n) mma_commit_warp(lead, &sm->o_full[i]);
                 mma_commit_warp(lead, &sm->v_empty[i]);
                 if (j + 1 < n) {
@@ -347,15 +347,13 @@ __device__ __forceinline__ void mma_role(const KvAttnArgs& a, Bars* sm, const ui
             if (ok && next < n1) ok = k_full(next);
             if (!ok) break;
             if (j < n0) {
-                ok = wait(&sm->p_full[0], (uint32_t)j & 1u);
+                ok = output(0, j, j);
                 if (!ok) break;
-                output(0, j, j == 0);
                 if (next == n0) mma_commit_warp(lead, &sm->o_full[0]);
                 if (next < n0) scores(0, 0, next);
             }
-            ok = wait(&sm->p_full[1], (uint32_t)j & 1u);
+            ok = output(1, j, j);
             if (!ok) break;
-            output(1, j, j == 0);
             if (next == n1) mma_commit_warp(lead, &sm->o_full[1]);
             mma_commit_warp(lead, &sm->v_empty[j & 1]);
             if (next < n1) {
@@ -370,56 +368,49 @@ __device__ __forceinline__ void mma_role(const KvAttnArgs& a, Bars* sm, const ui
 }
 
 // --------------------------------------------------------------- softmax
-// Thread t of 128 (a row of slot i), half h of the keys and of dim.
+// Thread t of 128: a row of slot i.
 template <int D>
-__device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, Tops* tops, uint8_t* q, uint8_t* tiles,
-                                             uint32_t tmem, int i, int h, int t) {
+__device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint8_t* q, uint8_t* tiles, uint32_t tmem,
+                                             int i, int t) {
     const Work& w = sm->work;
-    const int lane = t & 31, warp = 8 * i + 4 * h + (t >> 5), partner = warp ^ 4;
-    const uint32_t pair = 1u + 4 * i + (t >> 5);  // named barrier of the two warps that share rows
+    const int lane = t & 31, warp = 4 * i + (t >> 5);
     const bool dual = w.dual != 0;
     const int row = w.r0 + (dual ? 0 : i * kRows) + t;
     const bool in = row < w.rows;
     // Rows past the last one compute on zeros and are not written.
-    const int limit = (in ? key_limit(w.r.len - w.r.n + row / a.group, w.r.len, a.frame) : w.r.len) - w.k0 - 64 * h;
+    const int limit = (in ? key_limit(w.r.len - w.r.n + row / a.group, w.r.len, a.frame) : w.r.len) - w.k0;
     volatile int* abort = &sm->abort;
     float c;  // softmax scale * log2(e) / q's scale
     {
         const int token = in ? row / a.group : 0, qh = w.head * a.group + (in ? row % a.group : 0);
         const uint16_t* src = a.q.ptr + (int64_t)(w.r.first + token) * a.q.token_stride + (int64_t)qh * a.q.head_stride;
-        uint4 v[D / 16];
+        uint4 v[D / 8];
         uint32_t top = 0;
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
+        for (int k = 0; k < D / 8; ++k) {
             v[k] = make_uint4(0, 0, 0, 0);
-            if (in) v[k] = *reinterpret_cast<const uint4*>(src + (h * (D / 16) + k) * 8);
+            if (in) v[k] = *reinterpret_cast<const uint4*>(src + k * 8);
             top = absmax8(v[k], top);
         }
-        top = fold_halves(top);
-        tops->v[i][h][t] = __uint_as_float(top);
-        named_barrier_sync(pair, 64);
-        top = max(top, __float_as_uint(*(volatile float*)&tops->v[i][h ^ 1][t]));
-        const int e = q_exponent(top);
+        const int e = q_exponent(fold_halves(top));
         const float f = pow2f(e);
         c = a.scale_log2 * pow2f(-e);
         if (!dual || i == 0) {
             uint8_t* dst = q + i * Tile<D>::BYTES + t * 128;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-                const int p = h * (D / 16) + k;
+            for (int k = 0; k < D / 8; ++k) {
                 uint32_t* y = &v[k].x;
 #pragma unroll
                 for (int z = 0; z < 4; ++z) y[z] = pack_f16x2(bf16_lo(y[z]) * f, bf16_hi(y[z]) * f);
-                *reinterpret_cast<uint4*>(dst + (p >> 3) * Tile<D>::HALF + (((p & 7) ^ (t & 7)) << 4)) = v[k];
+                *reinterpret_cast<uint4*>(dst + (k >> 3) * Tile<D>::HALF + (((k & 7) ^ (t & 7)) << 4)) = v[k];
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->q_full[i]);
         }
-        named_barrier_sync(pair, 64);  // tops may be written again
     }
     const uint32_t lanes = (uint32_t)(t >> 5) << 21;  // this warp's TMEM lanes: (t / 32) * 32 << 16
-    const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + 2 * kKeys + i * D + h * (D / 2);
+    const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + 2 * kKeys + i * D;
     const int n = w.n[i];
     float m = kNegInf, l = 0.0f;
     int v_ref = -120;  // O is in units of 2^v_ref
@@ -427,57 +418,47 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, Tops
     for (int j = 0; j < n; ++j) {
         const int g = dual ? 2 * j + i : j;
         ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm->s_full[i], (uint32_t)j & 1u, abort, a.err));
-        uint32_t s[2][32];
-        float f[4], tile_top = kNegInf;  // f: score factors of 16 keys each
-        if (ok) {
-            tc_fence_after();
-            tmem_ld_32x32b_x32(s_addr + 64 * h, s[0]);
-            tmem_ld_32x32b_x32(s_addr + 64 * h + 32, s[1]);
-            const float4 ks = *reinterpret_cast<const float4*>(&sm->k_scale[g % kRing][4 * h]);
-            // Not 0: a masked score of -inf stays one.
-            f[0] = fmaxf(c * ks.x, 0x1p-126f), f[1] = fmaxf(c * ks.y, 0x1p-126f);
-            f[2] = fmaxf(c * ks.z, 0x1p-126f), f[3] = fmaxf(c * ks.w, 0x1p-126f);
-            const int seen = limit - g * kKeys;  // this row sees columns below it
-            const uint32_t bad = *(volatile uint32_t*)&sm->bad[g % kRing];
-            const bool mask = __any_sync(0xffffffffu, seen < 64) || bad;
-            tmem_wait_ld();
-            tmem_tie32(s[0]);
-            tmem_tie32(s[1]);
-            if (mask) {
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[4][32];
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(s_addr + 32 * k, s[k]);
+        float f[8];  // score factors of 16 keys each; not 0: a masked score of -inf stays one
 #pragma unroll
-                    for (int x = 0; x < 32; ++x)
-                        if (32 * k + x >= seen || (bad >> ((64 * h + 32 * k + x) >> a.c.block_log2) & 1u))
-                            s[k][x] = __float_as_uint(kNegInf);
-            }
-            float top[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z) {
-                const uint32_t* y = &s[z >> 1][(z & 1) * 16];
-                float u0 = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
-                float u1 = max3(__uint_as_float(y[3]), __uint_as_float(y[4]), __uint_as_float(y[5]));
-#pragma unroll
-                for (int x = 6; x < 14; x += 4) {
-                    u0 = max3(u0, __uint_as_float(y[x]), __uint_as_float(y[x + 1]));
-                    u1 = max3(u1, __uint_as_float(y[x + 2]), __uint_as_float(y[x + 3]));
-                }
-                u0 = max3(u0, __uint_as_float(y[14]), __uint_as_float(y[15]));
-                top[z] = fmaxf(u0, u1) * f[z];
-            }
-            tile_top = fmaxf(max3(top[0], top[1], top[2]), top[3]);
-            tops->v[i][h][t] = tile_top;
-        } else if (lane == 0) {
-            *(volatile int*)&sm->failed[warp] = 1;
+        for (int k = 0; k < 2; ++k) {
+            const float4 ks = *reinterpret_cast<const float4*>(&sm->k_scale[g % kRing][4 * k]);
+            f[4 * k] = fmaxf(c * ks.x, 0x1p-126f), f[4 * k + 1] = fmaxf(c * ks.y, 0x1p-126f);
+            f[4 * k + 2] = fmaxf(c * ks.z, 0x1p-126f), f[4 * k + 3] = fmaxf(c * ks.w, 0x1p-126f);
         }
-        // Both warps have read their scores (P will overwrite them).
-        named_barrier_sync(pair, 64);
-        if (!ok || *(volatile int*)&sm->failed[partner]) {
-            ok = false;
-            break;
-        }
-        tile_top = fmaxf(tile_top, *(volatile float*)&tops->v[i][h ^ 1][t]);
+        const int seen = limit - g * kKeys;  // this row sees columns below it
+        const uint32_t bad = *(volatile uint32_t*)&sm->bad[g % kRing];
         const int r = *(volatile int*)&sm->v_ref[g % kRing];
+        const bool mask = __any_sync(0xffffffffu, seen < kKeys) || bad;
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tmem_tie32(s[k]);
+        if (mask) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int x = 0; x < 32; ++x)
+                    if (32 * k + x >= seen || (bad >> ((32 * k + x) >> a.c.block_log2) & 1u))
+                        s[k][x] = __float_as_uint(kNegInf);
+        }
+        float tile_top = kNegInf;
+#pragma unroll
+        for (int z = 0; z < 8; ++z) {
+            const uint32_t* y = &s[z >> 1][(z & 1) * 16];
+            float u0 = max3(__uint_as_float(y[0]), __uint_as_float(y[1]), __uint_as_float(y[2]));
+            float u1 = max3(__uint_as_float(y[3]), __uint_as_float(y[4]), __uint_as_float(y[5]));
+#pragma unroll
+            for (int x = 6; x < 14; x += 4) {
+                u0 = max3(u0, __uint_as_float(y[x]), __uint_as_float(y[x + 1]));
+                u1 = max3(u1, __uint_as_float(y[x + 2]), __uint_as_float(y[x + 3]));
+            }
+            u0 = max3(u0, __uint_as_float(y[14]), __uint_as_float(y[15]));
+            tile_top = fmaxf(tile_top, fmaxf(u0, u1) * f[z]);
+        }
         if (__any_sync(0xffffffffu, tile_top > m + kLazy) || r != v_ref) {
             const float to = fmaxf(m, tile_top);
             const float down = to == kNegInf ? 1.0f : ex2_approx(m - to);
@@ -487,7 +468,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, Tops
             v_ref = r;
             if (j > 0) {  // O of the earlier tiles is complete: S came after it
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) {
+                for (int k = 0; k < D / 16; ++k) {
                     uint32_t o[16];
                     tmem_ld_32x32b_x16(o_addr + 16 * k, o);
                     tmem_wait_ld16(o);
@@ -501,64 +482,61 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, Tops
         const f32x2_t neg2 = f2_pack(neg, neg);
         f32x2_t sum[2] = {f2_pack(l, 0.0f), f2_pack(0.0f, 0.0f)};
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint32_t p[16];
+        for (int half = 0; half < 2; ++half) {
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-                const float fx = f[2 * k + (x >> 3)];
-                const float2 e = f2_unpack(f2_fma(
-                    f2_pack(__uint_as_float(s[k][2 * x]), __uint_as_float(s[k][2 * x + 1])), f2_pack(fx, fx), neg2));
-                const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
-                sum[x & 1] = f2_add(sum[x & 1], f2_pack(p0, p1));
-                p[x] = pack_f16x2(p0, p1);
+            for (int k = 2 * half; k < 2 * half + 2; ++k) {
+                uint32_t p[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    const float fx = f[2 * k + (x >> 3)];
+                    const float2 e = f2_unpack(
+                        f2_fma(f2_pack(__uint_as_float(s[k][2 * x]), __uint_as_float(s[k][2 * x + 1])), f2_pack(fx, fx), neg2));
+                    const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
+                    sum[x & 1] = f2_add(sum[x & 1], f2_pack(p0, p1));
+                    p[x] = pack_f16x2(p0, p1);
+                }
+                tmem_st_32x32b_x16(s_addr + 16 * k, p);
             }
-            tmem_st_32x32b_x16(s_addr + 32 * h + 16 * k, p);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm->p_full[i][half]);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->p_full[i]);
         const float2 t2 = f2_unpack(f2_add(sum[0], sum[1]));
         l = t2.x + t2.y;
     }
     if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm->o_full[i], 0, abort, a.err));
     tc_fence_after();
-    // The row's sum over both halves.
-    if (ok) tops->v[i][h][t] = l;
-    if (!ok && lane == 0) *(volatile int*)&sm->failed[warp] = 1;
-    named_barrier_sync(pair, 64);
-    if (*(volatile int*)&sm->failed[partner]) ok = false;
-    if (ok) l += *(volatile float*)&tops->v[i][h ^ 1][t];
 
     // Dual: slot 1 leaves its results in the buffers that only it has used (K's
     // and V's second; [4 dims][row] float4), slot 0 joins them.
-    float4* other = reinterpret_cast<float4*>(tiles + (h ? 3 : 1) * Tile<D>::BYTES);
-    float* meta = reinterpret_cast<float*>(q + Tile<D>::BYTES) + 3 * kRows * h;  // reference, sum, unit
+    auto other = [&](int d4) {
+        uint8_t* base = tiles + (d4 < D / 8 ? 1 : 3) * Tile<D>::BYTES;
+        return reinterpret_cast<float4*>(base) + (d4 < D / 8 ? d4 : d4 - D / 8) * kRows + t;
+    };
+    float* meta = reinterpret_cast<float*>(q + Tile<D>::BYTES);  // reference, sum, unit
     if (dual) {
-        if (i == 1) {
-            if (ok) {
-                meta[t] = m;
-                meta[kRows + t] = l;
-                meta[2 * kRows + t] = (float)v_ref;
-                if (n > 0) {
+        if (i == 1 && ok) {
+            meta[t] = m;
+            meta[kRows + t] = l;
+            meta[2 * kRows + t] = (float)v_ref;
+            if (n > 0) {
 #pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        uint32_t o[16];
-                        tmem_ld_32x32b_x16(o_addr + 16 * k, o);
-                        tmem_wait_ld16(o);
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t o[16];
+                    tmem_ld_32x32b_x16(o_addr + 16 * k, o);
+                    tmem_wait_ld16(o);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            other[(4 * k + x) * kRows + t] =
-                                make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                                            __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
-                    }
+                    for (int x = 0; x < 4; ++x)
+                        *other(4 * k + x) = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                                        __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
                 }
             }
-            if (!ok && lane == 0) *(volatile int*)&sm->failed[warp] = 1;
         }
-        named_barrier_sync(9, 512);
+        if (!ok && lane == 0) *(volatile int*)&sm->failed[warp] = 1;
+        named_barrier_sync(1, 256);  // reached whatever the waits said
         if (i == 1) return;
-        if (*(volatile int*)&sm->failed[warp + 8] || *(volatile int*)&sm->failed[partner + 8]) ok = false;
+        if (*(volatile int*)&sm->failed[warp + 4]) ok = false;
     }
     if (!ok) return;
     // out = (O x own + O' x theirs), O' of the other slot.
@@ -579,7 +557,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, Tops
     const int64_t tok = w.r.first + token;
     const int64_t flat = tok * a.q.heads + qh;
     const int64_t part = (int64_t)w.split * a.b.total * a.q.heads + flat;
-    if (in && h == 0) {
+    if (in) {
         const float lse = m == kNegInf ? kNegInf : m + lg2_approx(l);
         if (a.splits > 1)
             a.part_lse[part] = lse;
@@ -587,7 +565,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, Tops
             a.lse[flat] = lse * kLog2ToNat;
     }
 #pragma unroll
-    for (int k = 0; k < D / 32; ++k) {
+    for (int k = 0; k < D / 16; ++k) {
         uint32_t o[16];
         if (n > 0) {
             tmem_ld_32x32b_x16(o_addr + 16 * k, o);
@@ -602,7 +580,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, Tops
         if (theirs != 0.0f) {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const float4 z = other[(4 * k + x) * kRows + t];
+                const float4 z = *other(4 * k + x);
                 y[4 * x] = fmaf(z.x, theirs, y[4 * x]);
                 y[4 * x + 1] = fmaf(z.y, theirs, y[4 * x + 1]);
                 y[4 * x + 2] = fmaf(z.z, theirs, y[4 * x + 2]);
@@ -610,7 +588,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, Tops
             }
         }
         if (!in) continue;
-        const int d = h * (D / 2) + 16 * k;
+        const int d = 16 * k;
         if (a.splits > 1) {
             float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + d);
 #pragma unroll
@@ -633,8 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles(const __grid_consta
     extern __shared__ __align__(1024) uint8_t q[];
     uint8_t* tiles = q + 2 * Tile<D>::BYTES;  // K buffers 0, 1, V buffers 0, 1
     uint8_t* raw = tiles + 4 * Tile<D>::BYTES;
-    Tops* tops = reinterpret_cast<Tops*>(raw + 4 * Tile<D>::RAW);
-    Bars* sm = reinterpret_cast<Bars*>(tops + 1);
+    Bars* sm = reinterpret_cast<Bars*>(raw + 4 * Tile<D>::RAW);
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
@@ -673,26 +650,27 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles(const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm->q_full[i], 8);
+            mbar_init(&sm->q_full[i], 4);
             mbar_init(&sm->s_full[i], 1);
-            mbar_init(&sm->p_full[i], 8);
+            mbar_init(&sm->p_full[i][0], 4);
+            mbar_init(&sm->p_full[i][1], 4);
             mbar_init(&sm->o_full[i], 1);
-            mbar_init(&sm->k_full[i], 4);
+            mbar_init(&sm->k_full[i], 8);
             mbar_init(&sm->k_empty[i], 1);
-            mbar_init(&sm->v_full[i], 4);
+            mbar_init(&sm->v_full[i], 8);
             mbar_init(&sm->v_empty[i], 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sm->raw_full[i], 1);
-            mbar_init(&sm->raw_empty[i], 4);
+            mbar_init(&sm->raw_empty[i], 8);
         }
         mbar_init(&sm->drain, 1);
         sm->abort = 0;
-        for (int i = 0; i < 16; ++i) sm->failed[i] = 0;
+        for (int i = 0; i < 8; ++i) sm->failed[i] = 0;
         sm->work = w;
         fence_mbarrier_init();
     }
-    if (warp == 21) {
+    if (warp == 17) {
         tmem_alloc(&sm->tmem, Tile<D>::TMEM_COLS);
         tmem_relinquish();
     }
@@ -701,23 +679,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles(const __grid_consta
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, sm->tmem, 0);
 
-    if (warp < 16) {
+    if (warp < 8) {
         regs_inc<kRegsSoftmax>();
-        softmax_role<D>(a, sm, tops, q, tiles, tmem, warp >> 3, (warp >> 2) & 1, threadIdx.x & 127);
-    } else if (warp < 20) {
-        regs_inc<kRegsConvert>();
-        convert_role<D>(a, sm, raw, tiles, threadIdx.x & 127);
+        softmax_role<D>(a, sm, q, tiles, tmem, warp >> 2, threadIdx.x & 127);
+    } else if (warp < 16) {
+        regs_dec<kRegsConvert>();
+        convert_role<D>(a, sm, raw, tiles, threadIdx.x & 255);
     } else {
         regs_dec<kRegsOther>();
-        if (warp == 20)
+        if (warp == 16)
             load_role<D>(a, sm, raw, lane);
-        else if (warp == 21)
+        else if (warp == 17)
             mma_role<D>(a, sm, q, tiles, tmem);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 21) {
+    if (warp == 17) {
         tc_fence_after();
         tmem_dealloc(tmem, Tile<D>::TMEM_COLS);
     }
