@@ -34,6 +34,8 @@
 //
 // Bound: HBM, 2 bytes per token, kv head and dim; a granule's loads are issued
 // one granule ahead (4 KB in flight per warp at dim 128).
+#include <algorithm>
+
 #include "attention.cuh"
 #include "fp8_codec.cuh"
 
@@ -484,24 +486,43 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
 
 }  // namespace
 
-// Cutting a call: up to 16 rows per request go to kv_attn_rows (8 or 16 rows
-// per CTA), more to the tcgen05 kernel (256). Then, while the CTAs would not
-// fill the GPU (four per SM, or one), the keys are cut into ranges of at least
-// 256 (512).
+// Cutting a call. Up to 16 rows per request (new tokens x heads of a group) go
+// to kv_attn_rows, 8 or 16 to a CTA; more than that to the tcgen05 kernel, 256
+// to a CTA, unless the keys that kv_attn_rows would walk (once for every 16
+// rows) are few, where its shorter start wins: 64 rows x 16 heads over 100
+// tokens take 6.5 us there and 9.8 here, 24 rows x 64 over 4000 44 and 38, x 16
+// over 32760 84 and 57.
+// Then the keys are cut into ranges whose results kv_attn_join joins:
+//  - kv_attn_rows: until four CTAs run on every SM (one wave), with ranges of
+//    at least 256 keys and at most 64 of them; beyond one wave, ranges of
+//    about 1024 keys while they are at most 16 CTAs per SM, which even out
+//    requests of different lengths. 16 heads over 1000 tokens take 8.3 us in 4
+//    ranges and 10.8 in 2; 32 x 8 over 4000 50.9 us in 4 ranges, 53.4 in 8 and
+//    59.2 in 2; 32 requests of 100 .. 16001 tokens 103 us in 10, 157 in 2.
+//  - tcgen05 (one CTA per SM): only while they fill at most half of the SMs.
+//    More than that is left in one piece: 1560 rows x 16 heads are 112 CTAs on
+//    148 SMs, 485 us, and 522 us cut in four, although that fills the last
+//    wave; the GPU is at its power limit, so idle SMs let the others clock
+//    higher, and every range pays its CTAs' start and the join's traffic.
 KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads, int num_sms) {
     KvAttnPlan p{};
     const int64_t rows = (int64_t)b.max_new * (q_heads / c.heads);
-    p.tensor = rows > 16;
-    p.rows_per_tile = rows <= 8 ? 8 : rows <= 16 ? 16 : 256;
+    p.tensor = rows > 16 && (double)b.n * c.heads * (double)((rows + 15) / 16) * b.max_kv > 262144.0;
+    p.rows_per_tile = p.tensor ? 256 : rows <= 8 ? 8 : 16;
     const int64_t tiles = (rows + p.rows_per_tile - 1) / p.rows_per_tile;
     p.row_tiles = (int32_t)(tiles < 1 ? 1 : tiles);
     const int64_t ctas = (int64_t)b.n * p.row_tiles * c.heads;
-    const int64_t fill = p.tensor ? num_sms : 16ll * num_sms;
-    const int64_t least = 512;
-    int64_t splits = p.tensor ? fill / ctas : (fill + ctas - 1) / ctas;
-    const int64_t most = (b.max_kv + least - 1) / least;
-    if (splits > most) splits = most;
-    if (splits < 1) splits = 1;
+    const int64_t kv = b.max_kv;
+    int64_t splits = 1, most = 1;
+    if (p.tensor) {
+        splits = num_sms / ctas;
+        most = (kv + 511) / 512;
+    } else {
+        const int64_t even = std::min<int64_t>((16ll * num_sms + ctas - 1) / ctas, (kv + 1023) / 1024);
+        splits = std::max<int64_t>(4ll * num_sms / ctas, even);
+        most = std::min<int64_t>((kv + 255) / 256, 64);
+    }
+    splits = std::max<int64_t>(1, std::min(splits, most));
     int64_t chunk = (b.max_kv + splits - 1) / splits;
     chunk = (chunk + 127) / 128 * 128;
     if (chunk < 128) chunk = 128;

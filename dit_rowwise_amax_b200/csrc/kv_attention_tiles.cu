@@ -18,16 +18,16 @@
 // brought along when r grows. A V block is exact down to 2^-15 of the largest,
 // and better than P's own rounding down to 2^-24.
 //
-// Warp roles (20 warps, one CTA per SM):
+// Warp roles (16 warps, one CTA per SM):
 //   0-3, 4-7   softmax of slot 0 and 1, a thread per row. P is handed over in
 //              two halves, so the first half's product runs under the second
 //              half's exponentials.
-//   8-15       decode 64 keys' codes at a time into the 128-byte-swizzled fp16
+//   8-11       decode 64 keys' codes at a time into the 128-byte-swizzled fp16
 //              layout the MMAs read (K: row = key, K-major; V: the same bytes
 //              read MN-major, so neither is transposed).
-//   16         looks block indices and scales up and bulk-copies the codes
+//   12         looks block indices and scales up and bulk-copies the codes
 //              (untiled: a block and head is one contiguous piece).
-//   17         issues the MMAs (the converged warp, one lane), owns TMEM.
+//   13         issues the MMAs (the converged warp, one lane), owns TMEM.
 // Shared memory at dim 128: Q 64 KB, two decoded K and two V tiles 128 KB,
 // four raw stages 32 KB. TMEM: S (P over it) 2 x 128 columns, O 2 x dim.
 //
@@ -49,13 +49,15 @@ namespace {
 
 constexpr int kRows = 128;  // rows of a slot = TMEM lanes
 constexpr int kKeys = 128;  // keys of a tile
-constexpr int kThreads = 640;
+constexpr int kThreads = 512;
 constexpr float kLazy = 8.0f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
-// Registers per thread by role, out of the launch's 640 x 96.
-constexpr int kRegsSoftmax = 168, kRegsConvert = 56, kRegsOther = 32;
-static_assert(256 * kRegsSoftmax + 256 * kRegsConvert + 128 * kRegsOther <= kThreads * 96, "register split");
+// Registers per thread by role, out of the launch's 512 x 128. The softmax holds
+// a row's 128 scores: with 168 registers it spilled and was 6% slower, and with
+// eight decoding warps there are no more to give it (4% slower at 176).
+constexpr int kRegsSoftmax = 200, kRegsConvert = 64, kRegsOther = 48;
+static_assert(256 * kRegsSoftmax + 128 * kRegsConvert + 128 * kRegsOther <= kThreads * 128, "register split");
 
 // What the roles of a CTA agree on.
 struct Work {
@@ -190,7 +192,19 @@ __device__ __forceinline__ void load_role(const KvAttnArgs& a, Bars* sm, uint8_t
 // ---------------------------------------------------------- decode codes
 template <int D>
 __device__ __forceinline__ void convert_role(const KvAttnArgs& a, Bars* sm, const uint8_t* raw, uint8_t* tiles, int t) {
-    constexpr int VPR = D / 16;  // 16-byte raw vectors per row
+    // Thread t turns 16 codes (16 bytes) of a raw row into two 16-byte pieces
+    // of a swizzled fp16 row, kIters times per stage, kRowStep rows apart. At
+    // dim 128 a quarter of a warp reads the first half of one row and the
+    // second half of the next: both that read and the writes then cover all
+    // banks once.
+    constexpr int kIters = D / 32, kRowStep = 2048 / D;
+    const int row = D == 128 ? 2 * (t >> 4) + (((t >> 2) ^ (t >> 3)) & 1) : t >> 2;
+    const int c16 = D == 128 ? t & 7 : t & 3;
+    const uint8_t* src = raw + row * D + c16 * 16;
+    const int piece = (c16 & 3) * 2;
+    const int to = (c16 >> 2) * Tile<D>::HALF + row * 128;
+    uint8_t* dst0 = tiles + to + ((piece ^ (row & 7)) << 4);
+    uint8_t* dst1 = tiles + to + (((piece + 1) ^ (row & 7)) << 4);
     const int tlog = a.c.block_log2;
     const int lane = t & 31;
     const int n = sm->work.tiles;
@@ -202,21 +216,33 @@ __device__ __forceinline__ void convert_role(const KvAttnArgs& a, Bars* sm, cons
         for (int v = 0; v < 2; ++v) {
             uint64_t* full = v ? &sm->v_full[buf] : &sm->k_full[buf];
             uint64_t* empty = v ? &sm->v_empty[buf] : &sm->k_empty[buf];
+            // Not unrolled: the roles' loops share the instruction caches (7% slower).
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 const int st = 2 * v + half;
                 bool ok = mbar_wait_bounded(&sm->raw_full[st], (uint32_t)(g & 1), abort, a.err);
                 if (half == 0) ok = ok && mbar_wait_bounded(empty, (uint32_t)((g >> 1) & 1) ^ 1u, abort, a.err);
                 if (!__all_sync(0xffffffffu, ok)) return;
-                const uint4* src = reinterpret_cast<const uint4*>(raw + st * Tile<D>::RAW);
-                uint8_t* dst = tiles + (2 * v + buf) * Tile<D>::BYTES + half * (64 * 128);
-                const int valid = keys - g * kKeys - half * 64;  // rows below it hold tokens
-                uint4 in[VPR / 4];
+                const int at = (2 * v + buf) * Tile<D>::BYTES + half * (64 * 128);
+                uint4 in[kIters];
+                uint32_t mul[kIters];
 #pragma unroll
-                for (int it = 0; it < VPR / 4; ++it) in[it] = src[it * 256 + t];
+                for (int it = 0; it < kIters; ++it) {
+                    in[it] = *reinterpret_cast<const uint4*>(src + st * Tile<D>::RAW + it * kRowStep * D);
+                    if (v) mul[it] = sm->v_mul[half][(row + it * kRowStep) >> tlog];
+                }
+                if (v) {
+                    // Rows without a token may hold NaN codes, which a p of 0 keeps
+                    // (K's only reach scores that are masked).
+                    const int valid = keys - g * kKeys - half * 64;
+                    if (valid < 64 || *(volatile uint32_t*)&sm->bad[g % kRing]) {
 #pragma unroll
-                for (int it = 0; it < VPR / 4; ++it) {
-                    const int i = it * 256 + t, row = i / VPR, c16 = i % VPR;
+                        for (int it = 0; it < kIters; ++it)
+                            if (row + it * kRowStep >= valid || mul[it] == 0) in[it] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+#pragma unroll
+                for (int it = 0; it < kIters; ++it) {
                     uint32_t o[8];
                     const uint32_t x[4] = {in[it].x, in[it].y, in[it].z, in[it].w};
 #pragma unroll
@@ -225,29 +251,15 @@ __device__ __forceinline__ void convert_role(const KvAttnArgs& a, Bars* sm, cons
                         o[2 * k + 1] = decode2(x[k] >> 16);
                     }
                     if (v) {
-                        // Rows without a token may hold NaN codes, which a p of 0
-                        // keeps (K's only reach scores that are masked).
-                        uint32_t mul = sm->v_mul[half][row >> tlog];
-                        if (row >= valid) mul = 0;
-                        const __half2 m = *reinterpret_cast<const __half2*>(&mul);
+                        const __half2 m = *reinterpret_cast<const __half2*>(&mul[it]);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&o[k]), m);
                             o[k] = *reinterpret_cast<const uint32_t*>(&y);
                         }
-                        if (mul == 0) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) o[k] = 0;
-                        }
                     }
-                    uint8_t* p = dst + (c16 >> 2) * Tile<D>::HALF + row * 128;
-                    const int y = row & 7, c = (c16 & 3) * 2;
-                    // Lanes of the two 64-dim halves write their pieces in opposite
-                    // order: the eight lanes of a phase then cover all banks.
-                    const bool swap = (c16 >> 2) & 1;
-                    const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-                    *reinterpret_cast<uint4*>(p + (((c + (swap ? 1 : 0)) ^ y) << 4)) = swap ? hi : lo;
-                    *reinterpret_cast<uint4*>(p + (((c + (swap ? 0 : 1)) ^ y) << 4)) = swap ? lo : hi;
+                    *reinterpret_cast<uint4*>(dst0 + at + it * kRowStep * 128) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4*>(dst1 + at + it * kRowStep * 128) = make_uint4(o[4], o[5], o[6], o[7]);
                 }
                 fence_proxy_async_smem();  // before the MMAs (and the next raw copy) touch it
                 __syncwarp();
@@ -655,14 +667,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles(const __grid_consta
             mbar_init(&sm->p_full[i][0], 4);
             mbar_init(&sm->p_full[i][1], 4);
             mbar_init(&sm->o_full[i], 1);
-            mbar_init(&sm->k_full[i], 8);
+            mbar_init(&sm->k_full[i], 4);
             mbar_init(&sm->k_empty[i], 1);
-            mbar_init(&sm->v_full[i], 8);
+            mbar_init(&sm->v_full[i], 4);
             mbar_init(&sm->v_empty[i], 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&sm->raw_full[i], 1);
-            mbar_init(&sm->raw_empty[i], 8);
+            mbar_init(&sm->raw_empty[i], 4);
         }
         mbar_init(&sm->drain, 1);
         sm->abort = 0;
@@ -670,7 +682,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles(const __grid_consta
         sm->work = w;
         fence_mbarrier_init();
     }
-    if (warp == 17) {
+    if (warp == 13) {
         tmem_alloc(&sm->tmem, Tile<D>::TMEM_COLS);
         tmem_relinquish();
     }
@@ -682,20 +694,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles(const __grid_consta
     if (warp < 8) {
         regs_inc<kRegsSoftmax>();
         softmax_role<D>(a, sm, q, tiles, tmem, warp >> 2, threadIdx.x & 127);
-    } else if (warp < 16) {
+    } else if (warp < 12) {
         regs_dec<kRegsConvert>();
-        convert_role<D>(a, sm, raw, tiles, threadIdx.x & 255);
+        convert_role<D>(a, sm, raw, tiles, threadIdx.x & 127);
     } else {
         regs_dec<kRegsOther>();
-        if (warp == 16)
+        if (warp == 12)
             load_role<D>(a, sm, raw, lane);
-        else if (warp == 17)
+        else if (warp == 13)
             mma_role<D>(a, sm, q, tiles, tmem);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 17) {
+    if (warp == 13) {
         tc_fence_after();
         tmem_dealloc(tmem, Tile<D>::TMEM_COLS);
     }
