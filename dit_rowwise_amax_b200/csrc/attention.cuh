@@ -23,7 +23,7 @@ struct RotaryArgs {
     int64_t M;
     int32_t n_axes, pos_float, interleaved;
     int32_t dim, pairs;       // pairs = rotated elements / 2
-    int32_t units;            // 4-pair (or 8-element copy) units of a head
+    int32_t units;            // threads per token: units of a head
     int32_t heads_per_thread;
     double turns[FP8DIT_ROTARY_MAX_DIM / 2];  // freqs / (2 pi)
     uint8_t axis[FP8DIT_ROTARY_MAX_DIM / 2];
@@ -96,7 +96,7 @@ __device__ __forceinline__ Request load_request(const KvBatchView& v, int b, con
     const bool ok = o0 >= 0 && o1 >= o0 && o1 <= v.total && o1 - o0 <= v.max_new && len >= 0 && len <= v.max_kv &&
                     !(needs_start && len < o1 - o0);
     if (!ok) {
-        if (threadIdx.x == 0) atomicOr(err.word, kDevErrIndex);
+        if (threadIdx.x + threadIdx.y == 0) atomicOr(err.word, kDevErrIndex);
         r.n = 0;
         r.len = 0;
     }
