@@ -578,6 +578,15 @@ def _on_device(device: torch.device, fn, *args) -> int:
         return fn(*args)
 
 
+# The current stream's handle without building a Stream object (2 us of a
+# decoding step's call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_handle(device: torch.device) -> int:
+    return _raw_stream(device.index) if _raw_stream is not None else torch.cuda.current_stream(device).cuda_stream
+
+
 def _heads(x: torch.Tensor, name: str, dim: Optional[int], device: Optional[torch.device]) -> _Heads:
     """[tokens, heads, dim] bf16 as the library sees it; any token and head
     stride that is a multiple of 8 elements."""
@@ -589,10 +598,15 @@ def _heads(x: torch.Tensor, name: str, dim: Optional[int], device: Optional[torc
     if dim is not None and d != dim:
         raise ValueError(f"{name} must have heads of {dim} elements (got {d})")
     s0, s1, s2 = x.stride()
-    if d > 1 and s2 != 1:
+    if s2 != 1 and d > 1:
         raise ValueError(f"{name}'s heads must be contiguous")
     # The stride of an axis of one element says nothing: torch may report any.
     return _Heads(x.data_ptr(), s0 if n > 1 else max(h, 1) * d, s1 if h > 1 else d, h, 0)
+
+
+def _new_like(x: torch.Tensor) -> torch.Tensor:
+    """An uninitialised contiguous tensor of x's shape, type and device."""
+    return torch.empty_like(x, memory_format=torch.contiguous_format)
 
 
 _NO_HEADS = _Heads(None, 0, 0, 0, 0)
@@ -621,7 +635,7 @@ def rotary_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Ten
     hq = _heads(q, "q", None, None)
     dev = q.device
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out = _new_like(q)
     elif q_out.shape != q.shape:
         raise ValueError("q_out must have q's shape")
     ho = hq if q_out is q else _heads(q_out, "q_out", dim, dev)
@@ -631,7 +645,7 @@ def rotary_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Ten
         if k.shape[0] != M:
             raise ValueError("q and k must have the same number of tokens")
         if k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+            k_out = _new_like(k)
         elif k_out.shape != k.shape:
             raise ValueError("k_out must have k's shape")
         hko = hk if k_out is k else _heads(k_out, "k_out", dim, dev)
@@ -650,8 +664,11 @@ def rotary_axes(q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Ten
             or 2 * freqs.numel() != sum(axis_dims)):
         raise ValueError(f"freqs must be contiguous float64 in host memory, {sum(axis_dims) // 2} of them")
     _check(_on_device(dev, load_library().fp8_rotary_axes, hq, hk, ho, hko, M, dim, positions.data_ptr(), kind,
-                      freqs.data_ptr(), (ctypes.c_int32 * n)(*axis_dims), n, 1 if interleaved else 0, _stream(dev)))
+                      freqs.data_ptr(), (ctypes.c_int32 * n)(*axis_dims), n, 1 if interleaved else 0, _stream_handle(dev)))
     return q_out, k_out
+
+
+_E4M3_DTYPES = (torch.uint8, torch.float8_e4m3fn)
 
 
 class KVCache(NamedTuple):
@@ -673,24 +690,28 @@ class KVCache(NamedTuple):
 
 def _kv_cache(cache: Union[KVCache, Sequence[torch.Tensor]]) -> Tuple[_KvCache, torch.device]:
     k, v, ks, vs = cache
-    if k.dim() != 4 or not k.is_cuda:
-        raise ValueError("the cache's codes must be [blocks, kv heads, block tokens, head dim] on a CUDA device")
     dev, shape = k.device, k.shape
-    for t in (k, v):
-        if t.dtype not in (torch.uint8, torch.float8_e4m3fn) or t.shape != shape or not t.is_contiguous() or t.device != dev:
-            raise ValueError("the cache's k and v must be contiguous E4M3FN codes of one shape on one device")
-    for t in (ks, vs):
-        if t.dtype != torch.float32 or t.shape != shape[:2] or not t.is_contiguous() or t.device != dev:
-            raise ValueError("the cache's scales must be contiguous float32 [blocks, kv heads] beside its codes")
-    return _KvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), *(shape[i] for i in (0, 1, 2, 3))), dev
+    if len(shape) != 4 or dev.type != "cuda":
+        raise ValueError("the cache's codes must be [blocks, kv heads, block tokens, head dim] on a CUDA device")
+    if (k.dtype not in _E4M3_DTYPES or v.dtype not in _E4M3_DTYPES or v.shape != shape or v.device != dev
+            or not k.is_contiguous() or not v.is_contiguous()):
+        raise ValueError("the cache's k and v must be contiguous E4M3FN codes of one shape on one device")
+    n, heads, tokens, dim = shape
+    if (ks.dtype is not torch.float32 or vs.dtype is not torch.float32 or ks.shape != shape[:2] or vs.shape != shape[:2]
+            or ks.device != dev or vs.device != dev or not ks.is_contiguous() or not vs.is_contiguous()):
+        raise ValueError("the cache's scales must be contiguous float32 [blocks, kv heads] beside its codes")
+    return _KvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n, heads, tokens, dim), dev
 
 
 def _kv_batch(block_table: torch.Tensor, kv_lens: torch.Tensor, offsets: torch.Tensor, total: int, max_new: int,
               max_kv: Optional[int], block_tokens: int, dev: torch.device) -> _KvBatch:
-    n = kv_lens.numel()
-    for t, name, shape in ((block_table, "block_table", None), (kv_lens, "kv_lens", (n,)), (offsets, "offsets", (n + 1,))):
-        if t.dtype != torch.int32 or not t.is_contiguous() or t.device != dev or (shape is not None and t.shape != shape):
-            raise ValueError(f"{name} must be contiguous int32 on {dev}, one row per request (offsets: one more)")
+    n, i32 = kv_lens.numel(), torch.int32
+    if (block_table.dtype is not i32 or kv_lens.dtype is not i32 or offsets.dtype is not i32 or kv_lens.dim() != 1
+            or offsets.dim() != 1 or offsets.numel() != n + 1 or block_table.device != dev or kv_lens.device != dev
+            or offsets.device != dev or not block_table.is_contiguous() or not kv_lens.is_contiguous()
+            or not offsets.is_contiguous()):
+        raise ValueError(f"block_table, kv_lens and offsets must be contiguous int32 on {dev}, kv_lens [requests], "
+                         "offsets [requests + 1]")
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table must be [requests, blocks per request]")
     width = block_table.shape[1]
@@ -717,7 +738,7 @@ def kv_cache_append(cache: Union[KVCache, Sequence[torch.Tensor]], k: torch.Tens
     if k.shape != v.shape:
         raise ValueError("k and v must have the same shape")
     b = _kv_batch(block_table, kv_lens, offsets, k.shape[0], max_new, None, c.block_tokens, dev)
-    _check(_on_device(dev, load_library().fp8_kv_cache_append, c, hk, hv, b, _stream(dev)))
+    _check(_on_device(dev, load_library().fp8_kv_cache_append, c, hk, hv, b, _stream_handle(dev)))
 
 
 def kv_cache_attention(q: torch.Tensor, cache: Union[KVCache, Sequence[torch.Tensor]], block_table: torch.Tensor,
@@ -742,7 +763,7 @@ def kv_cache_attention(q: torch.Tensor, cache: Union[KVCache, Sequence[torch.Ten
     total, heads, dim = q.shape
     b = _kv_batch(block_table, kv_lens, offsets, total, max_q, max_kv, c.block_tokens, dev)
     if out is None:
-        out = torch.empty((total, heads, dim), dtype=torch.bfloat16, device=dev)
+        out = _new_like(q)
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
     ho = _heads(out, "out", dim, dev)
@@ -757,7 +778,7 @@ def kv_cache_attention(q: torch.Tensor, cache: Union[KVCache, Sequence[torch.Ten
             raise ValueError(f"workspace must be a contiguous tensor on {dev}")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _check(_on_device(dev, L.fp8_kv_cache_attention, c, hq, b, ho, None if lse is None else lse.data_ptr(),
-                      dim ** -0.5 if scale is None else scale, causal, ws, ws_bytes, _stream(dev)))
+                      dim ** -0.5 if scale is None else scale, causal, ws, ws_bytes, _stream_handle(dev)))
     return (out, lse) if return_lse else out
 
 
