@@ -64,6 +64,7 @@ struct KvAttnArgs {
     int32_t frame;      // causal granularity, 0: none
     int32_t splits;     // key ranges per (row tile, kv head)
     int32_t chunk;      // keys per range (a multiple of 128 when splits > 1)
+    int32_t tail_last;  // 1: the last row tile is a short one and is launched last
     int32_t row_tiles;  // row tiles per request (rows = new tokens x group)
     float* part_o;      // splits > 1: [splits][total * q heads][dim], normalised
     float* part_lse;    // splits > 1: [splits][total * q heads], log2 units; -inf: no key seen
@@ -74,6 +75,7 @@ struct KvAttnArgs {
 struct KvAttnPlan {
     int32_t rows_per_tile, row_tiles, splits, chunk;
     bool tensor;  // the tcgen05 kernel
+    bool tail_last;
     size_t ws_bytes;
 };
 KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads, int num_sms);

@@ -499,11 +499,32 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
 //    requests of different lengths. 16 heads over 1000 tokens take 8.3 us in 4
 //    ranges and 10.8 in 2; 32 x 8 over 4000 50.9 us in 4 ranges, 53.4 in 8 and
 //    59.2 in 2; 32 requests of 100 .. 16001 tokens 103 us in 10, 157 in 2.
-//  - tcgen05 (one CTA per SM): only while they fill at most half of the SMs.
-//    More than that is left in one piece: 1560 rows x 16 heads are 112 CTAs on
-//    148 SMs, 485 us, and 522 us cut in four, although that fills the last
-//    wave; the GPU is at its power limit, so idle SMs let the others clock
-//    higher, and every range pays its CTAs' start and the join's traffic.
+//  - tcgen05 (one CTA per SM): the number of ranges with the earliest estimated
+//    end (tensor_cost).
+//
+// tensor_cost: full row tiles are dealt to the SMs first, row tiles of at most
+// 128 rows fill in after them; a CTA takes 9 us and 1.9 us per tile of 128 keys
+// (a short one 0.83 of that, it decodes every tile for itself), the join reads
+// and writes its partials. For 1560 rows x 16 heads over 32760 tokens it gives
+// 495, 517, 504, 505, 453, 470 us for 1 .. 6 ranges; measured 491, 512, 510,
+// 494, 447, 470.
+static double tensor_cost(int64_t full, int64_t small, double kv_tiles, double row_bytes, int64_t s, int sms) {
+    const double tile = 1.9 * kv_tiles / (double)s, t_full = tile + 9.0, t_small = 0.83 * tile + 9.0;
+    full *= s;
+    small *= s;
+    const int64_t rounds = full / sms, rest = full % sms, idle = sms - rest;
+    const double after = (double)(rounds + (rest > 0)) * t_full;  // every full one is done
+    // Short ones: all on the SMs that are idle meanwhile, or one there each and
+    // the others behind the full ones.
+    const double beside = (double)rounds * t_full + (double)((small + idle - 1) / idle) * t_small;
+    const int64_t later = small > idle ? small - idle : 0;
+    const double first = (double)rounds * t_full + (small > 0 ? t_small : 0.0);
+    const double behind = std::max(after, first) + (double)((later + sms - 1) / sms) * t_small;
+    double end = small == 0 ? after : std::min(std::max(after, beside), behind);
+    if (s > 1) end += 3.0 + row_bytes * 2.0 * (double)s / 5e6;  // 5 TB/s
+    return end;
+}
+
 KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads, int num_sms) {
     KvAttnPlan p{};
     const int64_t rows = (int64_t)b.max_new * (q_heads / c.heads);
@@ -515,8 +536,20 @@ KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads,
     const int64_t kv = b.max_kv;
     int64_t splits = 1, most = 1;
     if (p.tensor) {
-        splits = num_sms / ctas;
-        most = (kv + 511) / 512;
+        const int64_t rem = rows % 256, heads = (int64_t)b.n * c.heads;
+        const bool tail = rem > 0 && rem <= 128;
+        const int64_t full = heads * (p.row_tiles - (tail ? 1 : 0)), small = tail ? heads : 0;
+        const double kv_tiles = (double)((kv + 127) / 128), row_bytes = (double)b.total * q_heads * (c.dim + 1) * 4.0;
+        most = std::min<int64_t>((kv + 511) / 512, 32);
+        double best = tensor_cost(full, small, kv_tiles, row_bytes, 1, num_sms);
+        for (int64_t s = 2; s <= most; ++s) {
+            const double cost = tensor_cost(full, small, kv_tiles, row_bytes, s, num_sms);
+            if (cost < 0.97 * best) {
+                best = cost;
+                splits = s;
+            }
+        }
+        p.tail_last = tail && p.row_tiles > 1;
     } else {
         const int64_t even = std::min<int64_t>((16ll * num_sms + ctas - 1) / ctas, (kv + 1023) / 1024);
         splits = std::max<int64_t>(4ll * num_sms / ctas, even);
@@ -562,6 +595,7 @@ cudaError_t launch_kv_attention(const KvAttnPlan& p, KvAttnArgs& a, cudaStream_t
     a.splits = p.splits;
     a.chunk = p.chunk;
     a.row_tiles = p.row_tiles;
+    a.tail_last = p.tail_last;
     return a.c.dim == 64 ? launch_for<64>(p, a, stream) : launch_for<128>(p, a, stream);
 }
 

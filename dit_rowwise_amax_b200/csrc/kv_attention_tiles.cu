@@ -140,7 +140,21 @@ __device__ __forceinline__ void load_role(const KvAttnArgs& a, Bars* sm, uint8_t
     int page = fetch_page(), next = fetch_page();
     float sk = fetch_scale(a.c.ks, page), sv = fetch_scale(a.c.vs, page);
     int v_ref = -120;
-    int done = 0;  // raw stages filled
+    // One raw stage: K's two halves, V's two halves.
+    auto mine = [&](int st) { return T == 128 ? lane == 0 : lane < per_tile && ((lane << tlog) >> 6) == (st & 1); };
+    const int key = (lane << tlog) & 63;  // first key of this lane's copy in its stage
+    auto copy = [&](int st) {
+        if (!mine(st) || page < 0) return;
+        const int64_t slot = (int64_t)page * a.c.heads + head;
+        bulk_load_g2s(raw + st * Tile<D>::RAW + key * D,
+                      (st >> 1 ? a.c.v : a.c.k) + ((slot << tlog) + (T == 128 ? 64 * (st & 1) : 0)) * D, bytes,
+                      &sm->raw_full[st]);
+    };
+    // The first tile's copies do not wait for its scales (the barriers count
+    // bytes that land before they are announced, too).
+    if (tiles > 0)
+        for (int st = 0; st < 4; ++st) copy(st);
+    int done = 0;  // raw stages announced
     for (int g = 0; g < tiles; ++g) {
         const int after = fetch_page();
         const float nk = fetch_scale(a.c.ks, next), nv = fetch_scale(a.c.vs, next);
@@ -150,19 +164,18 @@ __device__ __forceinline__ void load_role(const KvAttnArgs& a, Bars* sm, uint8_t
         uint32_t mul = page < 0 || e < -24 ? 0u : e >= -14 ? (uint32_t)(15 + e) << 10 : 1u << (24 + e);
         mul |= mul << 16;
         const float sk16 = __shfl_sync(0xffffffffu, sk, (lane << 4 >> tlog) & 31);
-        const int64_t slot = (int64_t)max(page, 0) * a.c.heads + head;
         bool fail = false;
-        for (int st = 0; st < 4; ++st) {  // K's two halves, V's two halves
-            const int v = st >> 1, half = st & 1;
-            const bool mine = T == 128 ? lane == 0 : lane < per_tile && ((lane << tlog) >> 6) == half;
-            const bool copy = mine && page >= 0;
-            const int count = __popc(__ballot_sync(0xffffffffu, copy));
-            if (!__all_sync(0xffffffffu, mbar_wait_bounded(&sm->raw_empty[st], (uint32_t)(g & 1) ^ 1u, abort, a.err))) {
-                fail = true;
-                break;
+        for (int st = 0; st < 4; ++st) {
+            const int count = __popc(__ballot_sync(0xffffffffu, mine(st) && page >= 0));
+            if (g > 0) {
+                if (!__all_sync(0xffffffffu,
+                                mbar_wait_bounded(&sm->raw_empty[st], (uint32_t)(g & 1) ^ 1u, abort, a.err))) {
+                    fail = true;
+                    break;
+                }
+                copy(st);
             }
-            const int key = (lane << tlog) & 63;  // first key of this lane's copy in the stage
-            if (v && mine) sm->v_mul[half][key >> tlog] = mul;
+            if (st >= 2 && mine(st)) sm->v_mul[st & 1][key >> tlog] = mul;
             if (st == 0) {
                 if (lane < kKeys / 16) sm->k_scale[g % kRing][lane] = sk16;
                 if (lane == 0) {
@@ -173,11 +186,6 @@ __device__ __forceinline__ void load_role(const KvAttnArgs& a, Bars* sm, uint8_t
             }
             __syncwarp();
             if (lane == 0) mbar_arrive_expect_tx(&sm->raw_full[st], (uint32_t)count * bytes);
-            __syncwarp();
-            if (copy)
-                bulk_load_g2s(raw + st * Tile<D>::RAW + key * D,
-                              (v ? a.c.v : a.c.k) + ((slot << tlog) + (T == 128 ? 64 * half : 0)) * D, bytes,
-                              &sm->raw_full[st]);
             ++done;
         }
         if (fail) break;
@@ -329,6 +337,7 @@ __device__ __forceinline__ void mma_role(const KvAttnArgs& a, Bars* sm, const ui
             mma_commit_warp(lead, &sm->k_empty[i]);
         }
         for (int j = 0; j < rounds && ok; ++j) {
+#pragma unroll 1
             for (int i = 0; i < 2 && ok; ++i) {
                 const int n = i ? n1 : n0, g = 2 * j + i;
                 if (j >= n) break;
@@ -392,30 +401,49 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
     // Rows past the last one compute on zeros and are not written.
     const int limit = (in ? key_limit(w.r.len - w.r.n + row / a.group, w.r.len, a.frame) : w.r.len) - w.k0;
     volatile int* abort = &sm->abort;
-    float c;  // softmax scale * log2(e) / q's scale
+    // Q, a warp its 32 rows: D / 8 lanes read a row (16 bytes each), so every
+    // load is whole lines, and agree on its largest |q|.
+    constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;
+    float c = 0.0f;  // softmax scale * log2(e) / q's scale, of this thread's row
     {
         const int token = in ? row / a.group : 0, qh = w.head * a.group + (in ? row % a.group : 0);
-        const uint16_t* src = a.q.ptr + (int64_t)(w.r.first + token) * a.q.token_stride + (int64_t)qh * a.q.head_stride;
-        uint4 v[D / 8];
-        uint32_t top = 0;
+        const int64_t own = in ? (int64_t)(w.r.first + token) * a.q.token_stride + (int64_t)qh * a.q.head_stride : -1;
+        const int part = lane % kLanes;
+        uint4 v[kLanes];
 #pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
+        for (int k = 0; k < kLanes; ++k) {
+            const int64_t at = __shfl_sync(0xffffffffu, own, k * kAtOnce + lane / kLanes);
             v[k] = make_uint4(0, 0, 0, 0);
-            if (in) v[k] = *reinterpret_cast<const uint4*>(src + k * 8);
-            top = absmax8(v[k], top);
+            if (at >= 0) v[k] = *reinterpret_cast<const uint4*>(a.q.ptr + at + part * 8);
         }
-        const int e = q_exponent(fold_halves(top));
-        const float f = pow2f(e);
-        c = a.scale_log2 * pow2f(-e);
-        if (!dual || i == 0) {
-            uint8_t* dst = q + i * Tile<D>::BYTES + t * 128;
+        // Step by step over all rows: each step is a chain of dependent shuffles.
+        uint32_t top[kLanes];
 #pragma unroll
-            for (int k = 0; k < D / 8; ++k) {
+        for (int k = 0; k < kLanes; ++k) top[k] = fold_halves(absmax8(v[k], 0));
+#pragma unroll
+        for (int z = 1; z < kLanes; z <<= 1)
+#pragma unroll
+            for (int k = 0; k < kLanes; ++k) top[k] = max(top[k], __shfl_xor_sync(0xffffffffu, top[k], z));
+        uint32_t mine = 0;
+#pragma unroll
+        for (int k = 0; k < kLanes; ++k) {
+            const uint32_t x = __shfl_sync(0xffffffffu, top[k], (lane % kAtOnce) * kLanes);
+            if (lane / kAtOnce == k) mine = x;
+        }
+        c = a.scale_log2 * pow2f(-q_exponent(mine));
+        if (!dual || i == 0) {
+#pragma unroll
+            for (int k = 0; k < kLanes; ++k) {
+                const float f = pow2f(q_exponent(top[k]));
+                const int r = (t & 96) + k * kAtOnce + lane / kLanes;
                 uint32_t* y = &v[k].x;
 #pragma unroll
                 for (int z = 0; z < 4; ++z) y[z] = pack_f16x2(bf16_lo(y[z]) * f, bf16_hi(y[z]) * f);
-                *reinterpret_cast<uint4*>(dst + (k >> 3) * Tile<D>::HALF + (((k & 7) ^ (t & 7)) << 4)) = v[k];
+                *reinterpret_cast<uint4*>(q + i * Tile<D>::BYTES + r * 128 + (part >> 3) * Tile<D>::HALF +
+                                          (((part & 7) ^ (r & 7)) << 4)) = v[k];
             }
+        }
+        if (!dual || i == 0) {
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->q_full[i]);
@@ -449,13 +477,22 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
         tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < 4; ++k) tmem_tie32(s[k]);
-        if (mask) {
+        if (__builtin_expect(mask, 0)) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
                 for (int x = 0; x < 32; ++x)
-                    if (32 * k + x >= seen || (bad >> ((32 * k + x) >> a.c.block_log2) & 1u))
-                        s[k][x] = __float_as_uint(kNegInf);
+                    if (32 * k + x >= seen) s[k][x] = __float_as_uint(kNegInf);
+            if (bad) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int x = 0; x < 32; x += 16)
+                        if (bad >> ((32 * k + x) >> a.c.block_log2) & 1u) {
+#pragma unroll
+                            for (int y = 0; y < 16; ++y) s[k][x + y] = __float_as_uint(kNegInf);
+                        }
+            }
         }
         float tile_top = kNegInf;
 #pragma unroll
@@ -471,7 +508,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
             u0 = max3(u0, __uint_as_float(y[14]), __uint_as_float(y[15]));
             tile_top = fmaxf(tile_top, fmaxf(u0, u1) * f[z]);
         }
-        if (__any_sync(0xffffffffu, tile_top > m + kLazy) || r != v_ref) {
+        if (__builtin_expect(__any_sync(0xffffffffu, tile_top > m + kLazy) || r != v_ref, 0)) {
             const float to = fmaxf(m, tile_top);
             const float down = to == kNegInf ? 1.0f : ex2_approx(m - to);
             const float fo = down * ex2_approx((float)(v_ref - r));
@@ -479,7 +516,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
             l *= down;
             v_ref = r;
             if (j > 0) {  // O of the earlier tiles is complete: S came after it
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < D / 16; ++k) {
                     uint32_t o[16];
                     tmem_ld_32x32b_x16(o_addr + 16 * k, o);
@@ -533,7 +570,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
             meta[kRows + t] = l;
             meta[2 * kRows + t] = (float)v_ref;
             if (n > 0) {
-#pragma unroll
+#pragma unroll 1
                 for (int k = 0; k < D / 16; ++k) {
                     uint32_t o[16];
                     tmem_ld_32x32b_x16(o_addr + 16 * k, o);
@@ -576,43 +613,68 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
         else if (a.lse)
             a.lse[flat] = lse * kLog2ToNat;
     }
+    // Through the slot's Q buffer (every product with it is done), so that rows
+    // leave in whole lines: 16-byte pieces, swizzled by the row. fp32 partials
+    // take two passes of half the dims.
+    uint8_t* stage = q + i * Tile<D>::BYTES;
+    const bool partial = a.splits > 1;
+    const int64_t own_at = !in ? -1 : partial ? part * D : tok * a.out.token_stride + (int64_t)qh * a.out.head_stride;
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-        uint32_t o[16];
-        if (n > 0) {
-            tmem_ld_32x32b_x16(o_addr + 16 * k, o);
-            tmem_wait_ld16(o);
-        } else {
+    for (int pass = 0; pass < 2; ++pass) {
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = 0;
-        }
-        float y[16];
+        for (int kk = 0; kk < D / 32; ++kk) {
+            const int k = pass * (D / 32) + kk;
+            uint32_t o[16];
+            if (n > 0) {
+                tmem_ld_32x32b_x16(o_addr + 16 * k, o);
+                tmem_wait_ld16(o);
+            } else {
 #pragma unroll
-        for (int x = 0; x < 16; ++x) y[x] = __uint_as_float(o[x]) * own;
-        if (theirs != 0.0f) {
+                for (int x = 0; x < 16; ++x) o[x] = 0;
+            }
+            float y[16];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const float4 z = *other(4 * k + x);
-                y[4 * x] = fmaf(z.x, theirs, y[4 * x]);
-                y[4 * x + 1] = fmaf(z.y, theirs, y[4 * x + 1]);
-                y[4 * x + 2] = fmaf(z.z, theirs, y[4 * x + 2]);
-                y[4 * x + 3] = fmaf(z.w, theirs, y[4 * x + 3]);
+            for (int x = 0; x < 16; ++x) y[x] = __uint_as_float(o[x]) * own;
+            if (theirs != 0.0f) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float4 z = *other(4 * k + x);
+                    y[4 * x] = fmaf(z.x, theirs, y[4 * x]);
+                    y[4 * x + 1] = fmaf(z.y, theirs, y[4 * x + 1]);
+                    y[4 * x + 2] = fmaf(z.z, theirs, y[4 * x + 2]);
+                    y[4 * x + 3] = fmaf(z.w, theirs, y[4 * x + 3]);
+                }
+            }
+            auto put = [&](int piece, uint4 x) {
+                *reinterpret_cast<uint4*>(stage + t * (2 * D) + ((piece ^ (t & 7)) << 4)) = x;
+            };
+            if (partial) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    put(4 * kk + x, make_uint4(__float_as_uint(y[4 * x]), __float_as_uint(y[4 * x + 1]),
+                                               __float_as_uint(y[4 * x + 2]), __float_as_uint(y[4 * x + 3])));
+            } else {
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    put(2 * k + x,
+                        make_uint4(pack_bf16x2(y[8 * x], y[8 * x + 1]), pack_bf16x2(y[8 * x + 2], y[8 * x + 3]),
+                                   pack_bf16x2(y[8 * x + 4], y[8 * x + 5]), pack_bf16x2(y[8 * x + 6], y[8 * x + 7])));
             }
         }
-        if (!in) continue;
-        const int d = 16 * k;
-        if (a.splits > 1) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + part * D + d);
-#pragma unroll
-            for (int x = 0; x < 4; ++x) dst[x] = make_float4(y[4 * x], y[4 * x + 1], y[4 * x + 2], y[4 * x + 3]);
-        } else {
-            uint4* dst =
-                reinterpret_cast<uint4*>(a.out.ptr + tok * a.out.token_stride + (int64_t)qh * a.out.head_stride + d);
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-                dst[x] = make_uint4(pack_bf16x2(y[8 * x], y[8 * x + 1]), pack_bf16x2(y[8 * x + 2], y[8 * x + 3]),
-                                    pack_bf16x2(y[8 * x + 4], y[8 * x + 5]), pack_bf16x2(y[8 * x + 6], y[8 * x + 7]));
+        if (!partial && pass == 0) continue;
+        __syncwarp();
+#pragma unroll 8
+        for (int k = 0; k < kLanes; ++k) {
+            const int r = k * kAtOnce + lane / kLanes, piece = lane % kLanes;
+            const int64_t at = __shfl_sync(0xffffffffu, own_at, r);
+            const uint4 x = *reinterpret_cast<const uint4*>(stage + ((t & 96) + r) * (2 * D) + ((piece ^ (r & 7)) << 4));
+            if (at < 0) continue;
+            if (partial)
+                *reinterpret_cast<uint4*>(a.part_o + at + pass * (D / 2) + piece * 4) = x;
+            else
+                *reinterpret_cast<uint4*>(a.out.ptr + at + piece * 8) = x;
         }
+        __syncwarp();
     }
 }
 
@@ -633,15 +695,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles(const __grid_consta
     }
 
     // Blocks in launch order: heads fastest, then requests, key ranges, and the
-    // row tiles from the last (which under a causal mask sees most) to the first.
+    // row tiles from the last (which under a causal mask sees most) to the first,
+    // a short last one at the end.
     Work w;
-    int64_t id = blockIdx.x;
-    w.head = (int)(id % a.c.heads);
-    id /= a.c.heads;
-    w.b = (int)(id % a.b.n);
-    id /= a.b.n;
-    w.split = (int)(id % a.splits);
-    const int tile = a.row_tiles - 1 - (int)(id / a.splits);
+    uint32_t id = blockIdx.x;
+    w.head = (int)(id % (uint32_t)a.c.heads);
+    id /= (uint32_t)a.c.heads;
+    w.b = (int)(id % (uint32_t)a.b.n);
+    id /= (uint32_t)a.b.n;
+    w.split = (int)(id % (uint32_t)a.splits);
+    const int idx = (int)(id / (uint32_t)a.splits) + a.tail_last;
+    const int tile = idx == a.row_tiles ? idx - 1 : a.row_tiles - 1 - idx;
     w.r = load_request(a.b, w.b, a.err, false);
     w.rows = w.r.n * a.group;
     w.r0 = tile * 2 * kRows;
