@@ -15,7 +15,8 @@ per-channel pre-quantised, K-major E4M3 weights -> scale / bias / bf16.
 Behind the Q / K / V projections: rotary positions with several axes
 (``rotary_axes``), a key / value cache in E4M3 with one power-of-two scale for
 each block of tokens and head (``KVCache``, ``kv_cache_append``) and attention
-over it (``kv_cache_attention``).
+over it (``kv_cache_attention``). Like the linears they serve inference: results
+carry no autograd history.
 """
 from __future__ import annotations
 
@@ -715,8 +716,11 @@ def _kv_batch(block_table: torch.Tensor, kv_lens: torch.Tensor, offsets: torch.T
     if block_table.dim() != 2 or block_table.shape[0] != n:
         raise ValueError("block_table must be [requests, blocks per request]")
     width = block_table.shape[1]
-    return _KvBatch(block_table.data_ptr(), kv_lens.data_ptr(), offsets.data_ptr(), total, n, width, max_new,
-                    width * block_tokens if max_kv is None else max_kv)
+    if max_kv is None:
+        max_kv = min(width * block_tokens, 1 << 30)
+    if not (0 <= max_new < 1 << 31 and 0 <= max_kv < 1 << 31):  # ctypes would cut them to 32 bits
+        raise ValueError("the bounds of a request's new and cached tokens must be in 0 .. 2^31 - 1")
+    return _KvBatch(block_table.data_ptr(), kv_lens.data_ptr(), offsets.data_ptr(), total, n, width, max_new, max_kv)
 
 
 def kv_cache_append(cache: Union[KVCache, Sequence[torch.Tensor]], k: torch.Tensor, v: torch.Tensor,
@@ -761,6 +765,8 @@ def kv_cache_attention(q: torch.Tensor, cache: Union[KVCache, Sequence[torch.Ten
     c, dev = _kv_cache(cache)
     hq = _heads(q, "q", c.head_dim, dev)
     total, heads, dim = q.shape
+    if not 0 <= causal < 1 << 31:
+        raise ValueError("causal must be 0, or the tokens of a frame")
     b = _kv_batch(block_table, kv_lens, offsets, total, max_q, max_kv, c.block_tokens, dev)
     if out is None:
         out = _new_like(q)

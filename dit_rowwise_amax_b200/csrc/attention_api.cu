@@ -177,7 +177,8 @@ fp8dit_status fp8_kv_cache_attention(const fp8dit_kv_cache* cache, const fp8dit_
     const DeviceInfo* dev = device_info();
     if (!dev) return FP8DIT_ERR_CUDA;
     const KvAttnPlan plan = kv_attn_plan(a.c, a.b, q->heads, dev->num_sms);
-    if ((int64_t)a.b.n * plan.row_tiles * plan.splits > INT32_MAX) return unsupported("too many row tiles");
+    if ((int64_t)a.b.n * plan.row_tiles * plan.splits * (plan.tensor ? a.c.heads : 1) > INT32_MAX)
+        return unsupported("too many row tiles");
     if (plan.ws_bytes > 0) {
         if (!workspace || !aligned(workspace, 16)) return invalid("this call needs a 16-byte aligned workspace");
         if (ws_bytes < plan.ws_bytes) return invalid("workspace smaller than fp8_kv_cache_attention_workspace_size");

@@ -500,8 +500,13 @@ fp8dit_status fp8_kv_cache_append(const fp8dit_kv_cache* cache, const fp8dit_hea
  * causal mask) min(kv_lens[b], (pos / g + 1) g) with pos the query's position
  * in its request: every query sees the frames up to its own whole. A row that
  * sees nothing is 0 (its lse -infinity). Scores, softmax sums and output are
- * held in fp32; p is rounded to bf16 for the product with V, the output once
- * to bf16.
+ * held in fp32. Both products run in fp16, in which the codes are exact: q is
+ * scaled by a power of two per row (what lies 2^-38 below the row's largest
+ * |q| is lost), the block scales are applied outside, p is rounded to fp16.
+ * With more than 16 rows (new tokens x query heads per kv head) a V block's
+ * values below 2^-24 of the request's and head's largest block scale lose
+ * bits, those of a block whose scale is below it count as 0. The output is
+ * rounded once to bf16.
  *   q, out     bf16 [total_tokens, q heads, head_dim]; q.heads % kv_heads == 0;
  *              out must not overlap the inputs.
  *   lse        fp32 [total_tokens, q heads], contiguous: natural log of the sum of exp(scale q . K_t); or NULL.

@@ -84,14 +84,21 @@ def attention(q, cache, table, kv_lens, offsets, scale, frame, good_page=None):
     """float64 (out, lse, bound) of every request's rows; rows of no request are
     NaN. bound: largest error that the operator's roundings allow per element.
 
-    With A = sum p |v| per element: rounding p to bf16 is off by half a step,
-    2^-8 relative, so the sum by 2^-8 A; the output's rounding adds 2^-8 |out|.
+    With A = sum p |v| per element: rounding p to fp16 is off by half a step,
+    2^-11 relative where p is a normal fp16, else by 2^-25 in units in which
+    the row's largest p (tensor cores) or largest p times block scale (few
+    rows) is at least 1; so the sum is off by at most 2^-11 A + 2^-25 n 448
+    max(p S) + 2^-25 n max(p) 448 max(S). V on the tensor cores is an fp16 in
+    units of the largest block scale: off by 2^-25 max(S). The output's
+    rounding to bf16 adds 2^-8 |out|.
     A score is an fp32 sum of D products, off by at most (D + 4) 2^-24 scale
-    sum |q k| =: e (D additions, the products' own and two scalings), plus the
-    2^-22 of an approximate exp2, its argument's rounding (2^-24 of a score
-    relative to the row's reference, |s - m| <= 2 max |s|, in log2 units): each
-    p is off by that relatively, numerator and denominator alike, hence
-    twice; the fp32 sums over n keys add n 2^-24 each."""
+    sum |q k| =: e (D additions, the products' own and two scalings; q's own
+    scaling to fp16 keeps all its bits down to 2^-38 of the row's largest:
+    D 2^-38 max |q| max |k| more), plus the 2^-22 of an approximate exp2, its
+    argument's rounding (2^-24 of a score relative to the row's reference, |s -
+    m| <= 2 max |s|, in log2 units, and of the block scale's exponent added to
+    it): each p is off by that relatively, numerator and denominator alike,
+    hence twice; the fp32 sums over n keys add n 2^-24 each."""
     k, v, ks, vs = cache
     t, dim = k.shape[2], k.shape[3]
     g = q.shape[1] // k.shape[1]
@@ -119,8 +126,13 @@ def attention(q, cache, table, kv_lens, offsets, scale, frame, good_page=None):
             if n:
                 mass = torch.where(seen, x.abs() @ kk.abs().T * scale, torch.zeros_like(s)).amax(1)
                 top = torch.where(seen, s.abs(), torch.zeros_like(s)).amax(1)
-                e = (dim + 4) * 2.0 ** -24 * mass + 2.0 ** -22 + 2 * 1.45 * 2.0 ** -24 * top
+                sv = vs[idx, h // g].double().repeat_interleave(t)[:n]
+                expo = sv.log2().abs().max()
+                e = (dim + 4) * 2.0 ** -24 * mass + 2.0 ** -22 + 2.0 ** -24 * (2 * 1.45 * top + expo)
+                e = e + dim * 2.0 ** -38 * x.abs().amax(1) * kk.abs().max() * scale
                 a = p @ vv.abs()
-                bound[lo:hi, h] = 2.0 ** -8 * (a + out[lo:hi, h].abs()) * 1.01 + (2 * e + 2 * n * 2.0 ** -24)[:, None] * a + 1e-38
+                floor = 2.0 ** -25 * (n * 448 * ((p * sv).amax(1) + p.amax(1) * sv.max()) + sv.max())
+                bound[lo:hi, h] = (2.0 ** -11 * a + 2.0 ** -8 * out[lo:hi, h].abs()) * 1.01 \
+                    + (2 * e + 2 * n * 2.0 ** -24)[:, None] * a + floor[:, None] + 1e-38
                 lse_bound[lo:hi, h] = e + n * 2.0 ** -24 + 2.0 ** -22 * (1 + z.abs().nan_to_num(posinf=0.0))
     return out, lse, bound, lse_bound

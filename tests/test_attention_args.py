@@ -118,6 +118,22 @@ def test_python_refuses_host_and_wrong_tensors():
         fp8.kv_cache_attention(q, c, *ints, max_q=1)
 
 
+def test_python_refuses_bounds_beyond_32_bits():
+    cpu = torch.device("cpu")
+    ints = [torch.zeros((1, 2), dtype=torch.int32), torch.zeros(1, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)]
+    for new, kv in ((1 << 32, 16), (-1, 16), (1, 1 << 32), (1, -1)):
+        with pytest.raises(ValueError):
+            fp8._kv_batch(*ints, 1, new, kv, 16, cpu)
+    assert fp8._kv_batch(*ints, 1, 1, None, 16, cpu).max_kv == 32
+    wide = torch.zeros((1, 1), dtype=torch.int32).expand(1, 1 << 26)  # 2^33 tokens: the default bound is cut to 2^30
+    with pytest.raises(ValueError):
+        fp8._kv_batch(wide, *ints[1:], 1, 1, None, 128, cpu)  # not contiguous
+    with pytest.raises(ValueError):
+        fp8._kv_batch(ints[0].long(), *ints[1:], 1, 1, None, 16, cpu)
+    with pytest.raises(ValueError):
+        fp8._kv_batch(ints[0], ints[1], ints[1], 1, 1, None, 16, cpu)
+
+
 def test_rotary_frequencies():
     f = fp8.rotary_frequencies((4, 8), 100.0)
     want = [1.0, 100.0 ** -0.5, 1.0, 100.0 ** -0.25, 100.0 ** -0.5, 100.0 ** -0.75]

@@ -121,6 +121,41 @@ def test_scales_over_the_whole_range(new, exponent):
         check((q.float() * 2.0 ** e).bfloat16(), cache, table, [n], [0, new], 0, max_q=new)
 
 
+@pytest.mark.parametrize("new", [1, 20, 300])
+@pytest.mark.parametrize("order", [1, -1])
+def test_value_scales_of_different_blocks(new, order):
+    """V blocks whose scales rise or fall by 2^-12 in all, met in either order:
+    every block keeps its own precision (tensor cores: exact to 2^-15 of the
+    largest), keys' scales likewise."""
+    g = torch.Generator("cuda").manual_seed(6)
+    heads, kv, dim, t = 4, 2, 128, 16
+    blocks = 52
+    cache = filled(blocks, t, kv, dim, g)
+    e = torch.arange(blocks, device="cuda") // 4
+    e = e if order > 0 else 12 - e
+    cache.v_scale.copy_(torch.exp2(-e.float())[:, None].expand(-1, kv))
+    cache.k_scale.copy_(torch.exp2(-6.0 - (torch.arange(blocks, device="cuda") % 5).float())[:, None].expand(-1, kv))
+    q = torch.randn((new, heads, dim), generator=g, device="cuda").bfloat16()
+    n = blocks * t - 5
+    check(q, cache, [list(range(blocks))], [n], [0, new], 0, max_q=new)
+    check(q, cache, [list(range(blocks))], [n], [0, new], 1, max_q=new)
+
+
+@pytest.mark.parametrize("new", [1, 40, 300])
+def test_one_block_much_smaller_and_all_zero_blocks(new):
+    """Blocks of zeros carry the smallest scale (2^-120) and weigh as any other;
+    a block 2^-40 below the others adds nothing visible."""
+    g = torch.Generator("cuda").manual_seed(7)
+    heads, kv, dim, t = 2, 1, 64, 32
+    cache = filled(20, t, kv, dim, g)
+    for b in (0, 3, 4, 19):
+        cache.v[b] = 0
+        cache.v_scale[b] = 2.0 ** -120
+    cache.v_scale[7] = 2.0 ** -48
+    q = torch.randn((new, heads, dim), generator=g, device="cuda").bfloat16()
+    check(q, cache, [list(range(20))], [20 * t], [0, new], 0, max_q=new)
+
+
 @pytest.mark.parametrize("new", [1, 16, 129])
 def test_scores_far_apart(new):
     """Rows whose maximum keeps rising by much, or is reached by one key only."""
@@ -302,6 +337,35 @@ def test_projection_rotary_append_attention():
                     assert torch.equal(cache[i].cpu()[table[b][j], :, :m], mirror[i][table[b][j], :, :m])
         check(q, cache, table, lens, offs, 60, max_q=max(new))
     assert fp8.device_error() == OK
+
+
+@pytest.mark.parametrize("new", [1, 12, 150])
+def test_calls_side_by_side_on_streams(new):
+    """Eight calls on four streams at once, workspaces allocated per call."""
+    g = torch.Generator("cuda").manual_seed(16)
+    cache = filled(130, 32, 2, 64, g)
+    table, tab, lens, offs = [list(range(130))], ints([list(range(130))]), ints([4100]), ints([0, new])
+    qs = [torch.randn((new, 4, 64), generator=g, device="cuda").bfloat16() for _ in range(8)]
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(4)], []
+    for i, q in enumerate(qs):
+        with torch.cuda.stream(streams[i % 4]):
+            outs.append(fp8.kv_cache_attention(q, cache, tab, lens, offs, max_q=new, causal=i % 2))
+    torch.cuda.synchronize()
+    for i, (q, out) in enumerate(zip(qs, outs)):
+        want, _, bound, _ = ref.attention(q, cache, table, [4100], [0, new], 0.125, i % 2)
+        assert bool(((out.double() - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("new", [40, 300])
+def test_split_ranges_under_a_causal_mask_with_empty_rows(new):
+    """Ranges that no row of a tile sees, and rows that see nothing at all."""
+    g = torch.Generator("cuda").manual_seed(17)
+    cache = filled(70, 64, 1, 128, g)
+    q = torch.randn((2 * new, 2, 128), generator=g, device="cuda").bfloat16()
+    table = [list(range(66)), list(range(66))]
+    check(q, cache, table, [4200, new - 7], [0, new, 2 * new], 1, max_q=new)
+    check(q, cache, table, [4200, new - 7], [0, new, 2 * new], 2000, max_q=new)
 
 
 def test_other_stream():
