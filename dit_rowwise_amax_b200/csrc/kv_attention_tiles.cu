@@ -694,18 +694,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attn_tiles(const __grid_consta
         return;
     }
 
-    // Blocks in launch order: heads fastest, then requests, key ranges, and the
-    // row tiles from the last (which under a causal mask sees most) to the first,
-    // a short last one at the end.
+    // CTAs in launch order: heads fastest, then key ranges, then a request's row
+    // tiles from the last (which under a causal mask sees most) to the first, a
+    // short last one at its end, then the requests, longest cache first (up to
+    // 32 of them): what takes longest begins first. (Requests of 1209 .. 6001
+    // tokens with row tiles outermost: 237 us, so: 223.)
     Work w;
     uint32_t id = blockIdx.x;
     w.head = (int)(id % (uint32_t)a.c.heads);
     id /= (uint32_t)a.c.heads;
-    w.b = (int)(id % (uint32_t)a.b.n);
-    id /= (uint32_t)a.b.n;
     w.split = (int)(id % (uint32_t)a.splits);
-    const int idx = (int)(id / (uint32_t)a.splits) + a.tail_last;
-    const int tile = idx == a.row_tiles ? idx - 1 : a.row_tiles - 1 - idx;
+    id /= (uint32_t)a.splits;
+    const int place = (int)(id % (uint32_t)a.row_tiles) + a.tail_last;
+    const int tile = place == a.row_tiles ? place - 1 : a.row_tiles - 1 - place;
+    w.b = (int)(id / (uint32_t)a.row_tiles);
+    if (a.b.n > 1 && a.b.n <= 32) {
+        const int len = lane < a.b.n ? a.b.kv_lens[lane] : INT32_MIN;
+        int before = 0;  // requests that go before this lane's
+        for (int k = 0; k < a.b.n; ++k) {
+            const int other = __shfl_sync(0xffffffffu, len, k);
+            before += other > len || (other == len && k < lane);
+        }
+        w.b = __ffs(__ballot_sync(0xffffffffu, lane < a.b.n && before == w.b)) - 1;
+    }
     w.r = load_request(a.b, w.b, a.err, false);
     w.rows = w.r.n * a.group;
     w.r0 = tile * 2 * kRows;

@@ -9,11 +9,12 @@
 //
 // Bound: HBM, 2 bytes read and 1 written per element. A row of threads owns
 // one block and head of K or of V, so the amax and the codes need one read: a
-// thread keeps 32 of the block's elements (four 16-byte loads in flight) in
-// registers between the two steps. That is 32 (16 x 64 elements) to 512
-// threads (128 x 128); small blocks put as many heads into a CTA as give it
-// 256 threads, whose slices of a token lie side by side (blocks of 16 x 64, 12
-// heads, 14441 tokens: 33.6 us with one head per CTA).
+// thread keeps 64 of the block's elements (eight 16-byte loads in flight) in
+// registers between the two steps (32 where a block and head has 1024). That
+// is 32 to 256 threads; small blocks put as many heads into a CTA as give it
+// 256, whose slices of a token lie side by side. 32760 tokens, 16 heads of 128:
+// 63.7 us, 6.3 TB/s (four loads per thread 73.6 us, two 171); blocks of 16 x
+// 64, 12 heads, 14441 tokens: 33.6 us with one head per CTA, 13.5 so.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -21,8 +22,6 @@
 
 namespace fp8dit {
 namespace {
-
-constexpr int kVecs = 4;  // 16-byte loads (8 elements) per thread
 
 // Exponent n of the scale that |x| <= amax (a non-negative bf16's bits) needs:
 // 448 = 1.75 x 2^8, so n = exponent - 8, one more if the mantissa is above 1.75.
@@ -37,9 +36,10 @@ __device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d) {
     return lo | hi << 16;
 }
 
-template <int D>
-__global__ void __launch_bounds__(512) kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
-    __shared__ uint32_t warp_max[16];
+// VECS: 16-byte loads (8 elements) per thread.
+template <int D, int VECS>
+__global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
+    __shared__ uint32_t warp_max[8];
     pdl_wait();
     pdl_trigger();
     const int T = 1 << a.c.block_log2;
@@ -67,17 +67,17 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const __grid_constant__ 
     const uint16_t* src = in.ptr + ((int64_t)r.first + base - start) * in.token_stride + h * in.head_stride;
 
     constexpr int VPR = D / 8;  // vectors per row
-    uint4 v[kVecs];
+    uint4 v[VECS];
     uint32_t m2 = 0;
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
+    for (int i = 0; i < VECS; ++i) {
         const int at = i * blockDim.x + threadIdx.x, row = at / VPR, col = at % VPR;
         v[i] = make_uint4(0, 0, 0, 0);
         if (works && row >= lo && row < hi)
             v[i] = *reinterpret_cast<const uint4*>(src + (int64_t)row * in.token_stride + col * 8);
     }
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
+    for (int i = 0; i < VECS; ++i) {
         m2 = absmax8(v[i], m2);
     }
     uint32_t m = fold_halves(m2);
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const __grid_constant__ 
     }
     const float inv = pow2f(-n);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
+    for (int i = 0; i < VECS; ++i) {
         const int at = i * blockDim.x + threadIdx.x, row = at / VPR;
         if (row < lo || row >= hi) continue;
         uint2 o;
@@ -130,12 +130,15 @@ __global__ void __launch_bounds__(512) kv_append_kernel(const __grid_constant__ 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
-    const int threads = (a.c.dim << a.c.block_log2) / (8 * kVecs);
+    const int elements = a.c.dim << a.c.block_log2;
+    const int vecs = elements >= 2048 ? 8 : 4;
+    const int threads = elements / (8 * vecs);
     const int per_cta = std::min(a.c.heads, std::max(1, 256 / threads));
     const dim3 grid((unsigned)((int64_t)a.b.n * a.touched), (unsigned)((a.c.heads + per_cta - 1) / per_cta), 2);
     const dim3 block(threads, per_cta);
-    return a.c.dim == 64 ? launch_pdl(kv_append_kernel<64>, grid, block, 0, stream, 1, a)
-                         : launch_pdl(kv_append_kernel<128>, grid, block, 0, stream, 1, a);
+    if (vecs == 4) return launch_pdl(kv_append_kernel<64, 4>, grid, block, 0, stream, 1, a);  // 16 x 64 elements
+    return a.c.dim == 64 ? launch_pdl(kv_append_kernel<64, 8>, grid, block, 0, stream, 1, a)
+                         : launch_pdl(kv_append_kernel<128, 8>, grid, block, 0, stream, 1, a);
 }
 
 }  // namespace fp8dit
