@@ -10,11 +10,11 @@
 // Bound: HBM, 2 bytes read and 1 written per element. A row of threads owns
 // one block and head of K or of V, so the amax and the codes need one read: a
 // thread keeps 64 of the block's elements (eight 16-byte loads in flight) in
-// registers between the two steps (32 where a block and head has 1024). That
-// is 32 to 256 threads; small blocks put as many heads into a CTA as give it
-// 256, whose slices of a token lie side by side. 32760 tokens, 16 heads of 128:
-// 63.7 us, 6.3 TB/s (four loads per thread 73.6 us, two 171); blocks of 16 x
-// 64, 12 heads, 14441 tokens: 33.6 us with one head per CTA, 13.5 so.
+// registers between the two steps. That is 16 (16 x 64 elements) to 256
+// threads; small blocks put as many heads into a CTA as give it 256, whose
+// slices of a token lie side by side. 32760 tokens, 16 heads of 128: 63 us,
+// 6.4 TB/s (four loads per thread 73.6 us, two 171); blocks of 16 x 64, 12
+// heads, 14441 tokens: 33.6 us with one head per CTA, 11.3 so.
 #include <algorithm>
 
 #include "attention.cuh"
@@ -22,6 +22,8 @@
 
 namespace fp8dit {
 namespace {
+
+constexpr int kVecs = 8;  // 16-byte loads (8 elements) per thread
 
 // Exponent n of the scale that |x| <= amax (a non-negative bf16's bits) needs:
 // 448 = 1.75 x 2^8, so n = exponent - 8, one more if the mantissa is above 1.75.
@@ -36,8 +38,7 @@ __device__ __forceinline__ uint32_t quant4(float a, float b, float c, float d) {
     return lo | hi << 16;
 }
 
-// VECS: 16-byte loads (8 elements) per thread.
-template <int D, int VECS>
+template <int D>
 __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ KvAppendArgs a) {
     __shared__ uint32_t warp_max[8];
     pdl_wait();
@@ -67,29 +68,28 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
     const uint16_t* src = in.ptr + ((int64_t)r.first + base - start) * in.token_stride + h * in.head_stride;
 
     constexpr int VPR = D / 8;  // vectors per row
-    uint4 v[VECS];
+    uint4 v[kVecs];
     uint32_t m2 = 0;
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) {
+    for (int i = 0; i < kVecs; ++i) {
         const int at = i * blockDim.x + threadIdx.x, row = at / VPR, col = at % VPR;
         v[i] = make_uint4(0, 0, 0, 0);
         if (works && row >= lo && row < hi)
             v[i] = *reinterpret_cast<const uint4*>(src + (int64_t)row * in.token_stride + col * 8);
     }
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-        m2 = absmax8(v[i], m2);
-    }
+    for (int i = 0; i < kVecs; ++i) m2 = absmax8(v[i], m2);
     uint32_t m = fold_halves(m2);
-    m = __reduce_max_sync(0xffffffffu, m);
-    const int warps = blockDim.x / 32;  // of this head
-    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.y * warps + (threadIdx.x >> 5)] = m;
+    for (int z = min(16, (int)blockDim.x / 2); z > 0; z >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, z));
+    const int warps = blockDim.x / 32;  // of this head (0: half a one)
+    if (warps > 1 && (threadIdx.x & 31) == 0) warp_max[threadIdx.y * warps + (threadIdx.x >> 5)] = m;
     // The block's old scale is read by every thread before any may replace it.
     const bool held = lo > 0;
     const float old = held ? *scale : 0.0f;
     __syncthreads();
     if (!works) return;
-    for (int w = 0; w < warps; ++w) m = max(m, warp_max[threadIdx.y * warps + w]);
+    if (warps > 1)
+        for (int w = 0; w < warps; ++w) m = max(m, warp_max[threadIdx.y * warps + w]);
     const int need = scale_exponent(m);
     int n = need;
     if (held) {
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
     }
     const float inv = pow2f(-n);
 #pragma unroll
-    for (int i = 0; i < VECS; ++i) {
+    for (int i = 0; i < kVecs; ++i) {
         const int at = i * blockDim.x + threadIdx.x, row = at / VPR;
         if (row < lo || row >= hi) continue;
         uint2 o;
@@ -130,15 +130,13 @@ __global__ void __launch_bounds__(256) kv_append_kernel(const __grid_constant__ 
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream) {
-    const int elements = a.c.dim << a.c.block_log2;
-    const int vecs = elements >= 2048 ? 8 : 4;
-    const int threads = elements / (8 * vecs);
-    const int per_cta = std::min(a.c.heads, std::max(1, 256 / threads));
+    const int threads = (a.c.dim << a.c.block_log2) / (8 * kVecs);
+    int per_cta = std::min(a.c.heads, std::max(1, 256 / threads));
+    if (threads == 16) per_cta += per_cta & 1;  // whole warps
     const dim3 grid((unsigned)((int64_t)a.b.n * a.touched), (unsigned)((a.c.heads + per_cta - 1) / per_cta), 2);
     const dim3 block(threads, per_cta);
-    if (vecs == 4) return launch_pdl(kv_append_kernel<64, 4>, grid, block, 0, stream, 1, a);  // 16 x 64 elements
-    return a.c.dim == 64 ? launch_pdl(kv_append_kernel<64, 8>, grid, block, 0, stream, 1, a)
-                         : launch_pdl(kv_append_kernel<128, 8>, grid, block, 0, stream, 1, a);
+    return a.c.dim == 64 ? launch_pdl(kv_append_kernel<64>, grid, block, 0, stream, 1, a)
+                         : launch_pdl(kv_append_kernel<128>, grid, block, 0, stream, 1, a);
 }
 
 }  // namespace fp8dit
