@@ -571,17 +571,20 @@ def scaled_linear_multi(layers: Sequence[FP8Linear], a: torch.Tensor,
     return list(ys)
 
 
+# Below the Python layers that each check for an initialised CUDA (the tensors
+# at hand show that it is), where this torch has them: the current device, and
+# the current stream's handle without building a Stream object (together 2.5 us
+# of a decoding step's call).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _on_device(device: torch.device, fn, *args) -> int:
     """Call a library entry with `device` as the current device."""
-    if device.index == torch.cuda.current_device():
+    if device.index == _current_device():
         return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
-
-
-# The current stream's handle without building a Stream object (2 us of a
-# decoding step's call), where this torch has it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_handle(device: torch.device) -> int:
@@ -591,18 +594,19 @@ def _stream_handle(device: torch.device) -> int:
 def _heads(x: torch.Tensor, name: str, dim: Optional[int], device: Optional[torch.device]) -> _Heads:
     """[tokens, heads, dim] bf16 as the library sees it; any token and head
     stride that is a multiple of 8 elements."""
-    if not isinstance(x, torch.Tensor) or x.dtype not in _BF16_DTYPES or x.dim() != 3:
+    strides = x.stride() if isinstance(x, torch.Tensor) else ()
+    if len(strides) != 3 or (x.dtype is not torch.bfloat16 and x.dtype not in _BF16_DTYPES):
         raise ValueError(f"{name} must be a bf16 tensor [tokens, heads, dim]")
     if not x.is_cuda or (device is not None and x.device != device):
         raise ValueError(f"{name} must be on {device if device is not None else 'a CUDA device'} (got {x.device})")
     n, h, d = x.shape
+    s0, s1, s2 = strides
     if dim is not None and d != dim:
         raise ValueError(f"{name} must have heads of {dim} elements (got {d})")
-    s0, s1, s2 = x.stride()
     if s2 != 1 and d > 1:
         raise ValueError(f"{name}'s heads must be contiguous")
     # The stride of an axis of one element says nothing: torch may report any.
-    return _Heads(x.data_ptr(), s0 if n > 1 else max(h, 1) * d, s1 if h > 1 else d, h, 0)
+    return _Heads(x.data_ptr(), s0 if n > 1 else (h or 1) * d, s1 if h > 1 else d, h, 0)
 
 
 def _new_like(x: torch.Tensor) -> torch.Tensor:
@@ -698,8 +702,10 @@ def _kv_cache(cache: Union[KVCache, Sequence[torch.Tensor]]) -> Tuple[_KvCache, 
             or not k.is_contiguous() or not v.is_contiguous()):
         raise ValueError("the cache's k and v must be contiguous E4M3FN codes of one shape on one device")
     n, heads, tokens, dim = shape
-    if (ks.dtype is not torch.float32 or vs.dtype is not torch.float32 or ks.shape != shape[:2] or vs.shape != shape[:2]
-            or ks.device != dev or vs.device != dev or not ks.is_contiguous() or not vs.is_contiguous()):
+    pair = shape[:2]
+    f32 = torch.float32
+    if (ks.dtype is not f32 or vs.dtype is not f32 or ks.shape != pair or vs.shape != pair or ks.device != dev
+            or vs.device != dev or not ks.is_contiguous() or not vs.is_contiguous()):
         raise ValueError("the cache's scales must be contiguous float32 [blocks, kv heads] beside its codes")
     return _KvCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n, heads, tokens, dim), dev
 
