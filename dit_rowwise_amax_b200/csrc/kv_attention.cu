@@ -490,9 +490,12 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
 // Cutting a call. Up to 16 rows per request (new tokens x heads of a group) go
 // to kv_attn_rows, 8 or 16 to a CTA; more than that to the tcgen05 kernel, 256
 // to a CTA, unless the keys that kv_attn_rows would walk (once for every 16
-// rows) are few, where its shorter start wins: 64 rows x 16 heads over 100
-// tokens take 6.5 us there and 9.8 here, 24 rows x 64 over 4000 44 and 38, x 16
-// over 32760 84 and 57.
+// rows, and a start and an end worth 384 keys) are few, where its shorter start
+// wins: 64 rows x 8 heads over 1024 tokens take 11.0 us there and 17.3 here,
+// x 128 over 128 13.6 and 11.3, x 128 over 2048 73 and 33; 32 x 148 over 256
+// 11.3 and 12.4, over 512 23.6 and 15.5. Over 221 such calls (1 to 148 heads,
+// 17 to 1600 rows, 128 to 4096 tokens) the faster of the two is taken or one
+// 0.6% slower on average, 21% at most.
 // Then the keys are cut into ranges whose results kv_attn_join joins:
 //  - kv_attn_rows: until four CTAs run on every SM (one wave), with ranges of
 //    at least 256 keys and at most 64 of them; beyond one wave, ranges of
@@ -529,7 +532,7 @@ static double tensor_cost(int64_t full, int64_t small, double kv_tiles, double r
 KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads, int num_sms) {
     KvAttnPlan p{};
     const int64_t rows = (int64_t)b.max_new * (q_heads / c.heads);
-    p.tensor = rows > 16 && (double)b.n * c.heads * (double)((rows + 15) / 16) * b.max_kv > 262144.0;
+    p.tensor = rows > 16 && (double)b.n * c.heads * (double)((rows + 15) / 16) * (b.max_kv + 384.0) > 216000.0;
     p.rows_per_tile = p.tensor ? 256 : rows <= 8 ? 8 : 16;
     const int64_t tiles = (rows + p.rows_per_tile - 1) / p.rows_per_tile;
     p.row_tiles = (int32_t)(tiles < 1 ? 1 : tiles);
