@@ -144,9 +144,10 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // is exact there and decoding is one instruction for two codes (four to bf16).
 // q is brought to [2^14, 2^15) by a power of two per row (q_exponent, from the
 // row's largest |q|), undone in the score; what lies 2^-38 below the row's
-// largest is lost, as in any fp32 sum of products.
+// largest is lost, as in any fp32 sum of products (the exponent's bounds: the
+// largest bf16 still comes below 2^15, rows below 2^-105 keep 2^119).
 __device__ __forceinline__ int q_exponent(uint32_t amax_bf16_bits) {
-    return max(-110, min(110, 14 + 127 - (int)(amax_bf16_bits >> 7)));
+    return max(-113, min(119, 14 + 127 - (int)(amax_bf16_bits >> 7)));
 }
 __device__ __forceinline__ float pow2f(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }  // -126 .. 127
 // log2 of a block's scale (a power of two).

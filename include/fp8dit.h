@@ -507,7 +507,8 @@ fp8dit_status fp8_kv_cache_append(const fp8dit_kv_cache* cache, const fp8dit_hea
  * values below 2^-24 of the request's and head's largest block scale lose
  * bits, those of a block whose scale is below it count as 0. The output is
  * rounded once to bf16.
- *   q, out     bf16 [total_tokens, q heads, head_dim]; q.heads % kv_heads == 0;
+ *   cache      no NaN codes or scales among a request's kv_lens[b] tokens; what lies behind them does not matter.
+ *   q, out     bf16 [total_tokens, q heads, head_dim]; q.heads % kv_heads == 0; q finite;
  *              out must not overlap the inputs.
  *   lse        fp32 [total_tokens, q heads], contiguous: natural log of the sum of exp(scale q . K_t); or NULL.
  *   scale      finite, > 0.

@@ -122,6 +122,19 @@ def test_scales_over_the_whole_range(new, exponent):
         check((q.float() * 2.0 ** e).bfloat16(), cache, table, [n], [0, new], 0, max_q=new)
 
 
+@pytest.mark.parametrize("new", [1, 9, 140])
+def test_queries_up_to_the_largest_bf16(new):
+    """Keys of blocks with the smallest scale bring them back near one."""
+    g = torch.Generator("cuda").manual_seed(5)
+    heads, kv, dim, t, n = 2, 1, 64, 16, 150
+    cache = filled(10, t, kv, dim, g)
+    cache.k_scale.fill_(2.0 ** -120)
+    q = (torch.randn((new, heads, dim), generator=g, device="cuda") * 2.0 ** 124).bfloat16()
+    q[:, 1, 5] = torch.finfo(torch.bfloat16).max
+    q[:, 0, 7] = -torch.finfo(torch.bfloat16).max
+    check(q, cache, [list(range(10))], [n], [0, new], 0, scale=2.0 ** -14, max_q=new)
+
+
 @pytest.mark.parametrize("new", [1, 20, 300])
 @pytest.mark.parametrize("order", [1, -1])
 def test_value_scales_of_different_blocks(new, order):
