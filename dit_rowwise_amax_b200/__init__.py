@@ -30,7 +30,7 @@ __all__ = [
     "E4M3FN", "E5M2", "Fp8DitError", "FP8Linear", "library_path", "load_library",
     "quantize_rowwise", "act_quantize_rowwise", "quantize_weight_per_channel", "quantize_per_tensor", "convert_state_dict",
     "scaled_linear_multi", "rotary_frequencies", "rotary_axes", "KVCache", "kv_cache_append", "kv_cache_attention",
-    "device_error", "selftest_expired_wait", "selftest_quotient", "as_float8",
+    "kv_cache_attention_plan", "device_error", "selftest_expired_wait", "selftest_quotient", "as_float8",
 ]
 
 E4M3FN = 0
@@ -121,6 +121,7 @@ def load_library():
     L.fp8_kv_cache_append.argtypes = [pc, ph, ph, pb, p]
     L.fp8_kv_cache_attention_workspace_size.argtypes = [pc, pb, i32]
     L.fp8_kv_cache_attention_workspace_size.restype = ctypes.c_size_t
+    L.fp8_kv_cache_attention_plan.argtypes = [pc, pb, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)]
     L.fp8_kv_cache_attention.argtypes = [pc, ph, pb, ph, p, ctypes.c_float, i32, p, ctypes.c_size_t, p]
     L.fp8dit_device_error.argtypes = [p]
     L.fp8dit_selftest_expired_wait.argtypes = [i64, p]
@@ -132,7 +133,7 @@ def load_library():
                  "fp8_scaled_linear_noalloc", "fp8_weight_only_linear", "fp8_scaled_linear_fused",
                  "fp8_linear_set_host_pipeline", "fp8_scaled_linear_host",
                  "fp8_linear_plan", "fp8_linear_set_workspace", "fp8_rotary_axes", "fp8_kv_cache_append",
-                 "fp8_kv_cache_attention", "fp8dit_device_error",
+                 "fp8_kv_cache_attention", "fp8_kv_cache_attention_plan", "fp8dit_device_error",
                  "fp8dit_selftest_expired_wait",
                  "fp8dit_selftest_quotient"):
         getattr(L, name).restype = st
@@ -792,6 +793,21 @@ def kv_cache_attention(q: torch.Tensor, cache: Union[KVCache, Sequence[torch.Ten
     _check(_on_device(dev, L.fp8_kv_cache_attention, c, hq, b, ho, None if lse is None else lse.data_ptr(),
                       dim ** -0.5 if scale is None else scale, causal, ws, ws_bytes, _stream_handle(dev)))
     return (out, lse) if return_lse else out
+
+
+def kv_cache_attention_plan(q: torch.Tensor, cache: Union[KVCache, Sequence[torch.Tensor]], block_table: torch.Tensor,
+                            kv_lens: torch.Tensor, offsets: torch.Tensor, max_q: int,
+                            max_kv: Optional[int] = None) -> Tuple[int, int]:
+    """How kv_cache_attention cuts a call of these sizes: (rows per thread
+    block, ranges of keys). Rows are new tokens times query heads per kv head;
+    256 of them belong to the tcgen05 kernel, 8 or 16 to the one for few rows."""
+    c, dev = _kv_cache(cache)
+    _heads(q, "q", c.head_dim, dev)
+    b = _kv_batch(block_table, kv_lens, offsets, q.shape[0], max_q, max_kv, c.block_tokens, dev)
+    rows, ranges = ctypes.c_int32(), ctypes.c_int32()
+    _check(_on_device(dev, load_library().fp8_kv_cache_attention_plan, c, b, q.shape[1], ctypes.byref(rows),
+                      ctypes.byref(ranges)))
+    return rows.value, ranges.value
 
 
 def device_error(device: Optional[torch.device] = None) -> int:

@@ -155,6 +155,26 @@ size_t fp8_kv_cache_attention_workspace_size(const fp8dit_kv_cache* cache, const
     return dev ? kv_attn_plan(c, b, q_heads, dev->num_sms).ws_bytes : 0;
 }
 
+fp8dit_status fp8_kv_cache_attention_plan(const fp8dit_kv_cache* cache, const fp8dit_kv_batch* batch, int32_t q_heads,
+                                          int32_t* rows_per_tile, int32_t* key_ranges) {
+    clear_error();
+    KvCacheView c{};
+    KvBatchView b{};
+    fp8dit_status st = check_cache(cache, &c);
+    if (st == FP8DIT_OK) st = check_batch(batch, c, &b);
+    if (st != FP8DIT_OK) return st;
+    if (q_heads <= 0 || q_heads % c.heads != 0) return invalid("q's heads must be a multiple of the cache's");
+    KvAttnPlan plan{};
+    if (!nothing(b)) {
+        const DeviceInfo* dev = device_info();
+        if (!dev) return FP8DIT_ERR_CUDA;
+        plan = kv_attn_plan(c, b, q_heads, dev->num_sms);
+    }
+    if (rows_per_tile) *rows_per_tile = plan.rows_per_tile;
+    if (key_ranges) *key_ranges = plan.splits;
+    return FP8DIT_OK;
+}
+
 fp8dit_status fp8_kv_cache_attention(const fp8dit_kv_cache* cache, const fp8dit_heads* q, const fp8dit_kv_batch* batch,
                                      const fp8dit_heads* out, float* lse, float scale, int32_t causal,
                                      void* workspace, size_t ws_bytes, fp8dit_stream_t stream) {

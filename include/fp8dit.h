@@ -519,6 +519,17 @@ fp8dit_status fp8_kv_cache_append(const fp8dit_kv_cache* cache, const fp8dit_hea
  */
 size_t fp8_kv_cache_attention_workspace_size(const fp8dit_kv_cache* cache, const fp8dit_kv_batch* batch,
                                              int32_t q_heads);
+
+/*
+ * How fp8_kv_cache_attention cuts a call of these sizes (they alone decide, the
+ * batch's device arrays are not read): rows_per_tile rows (new tokens x query
+ * heads per kv head) per thread block, 256 on the tcgen05 kernel, 8 or 16 on
+ * the one for few rows; key_ranges ranges of keys, joined by a second launch
+ * if more than 1. Both 0 for a call without rows. For reports and tests.
+ */
+fp8dit_status fp8_kv_cache_attention_plan(const fp8dit_kv_cache* cache, const fp8dit_kv_batch* batch, int32_t q_heads,
+                                          int32_t* rows_per_tile, int32_t* key_ranges);
+
 fp8dit_status fp8_kv_cache_attention(const fp8dit_kv_cache* cache, const fp8dit_heads* q, const fp8dit_kv_batch* batch,
                                      const fp8dit_heads* out, float* lse, float scale, int32_t causal,
                                      void* workspace, size_t ws_bytes, fp8dit_stream_t stream);
