@@ -585,7 +585,9 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
         const float2 t2 = f2_unpack(f2_add(sum[0], sum[1]));
         l = t2.x + t2.y;
     }
-    if (n > 0 && ok) ok = __all_sync(0xffffffffu, wait_for(&sm->o_full[i], 0, abort, a.err));
+    // The slot's O; without a key tile the slot's Q, whose buffer takes the rows
+    // on their way out: every warp of the slot has to have written its own.
+    if (ok) ok = __all_sync(0xffffffffu, wait_for(n > 0 ? &sm->o_full[i] : &sm->q_full[dual ? 0 : i], 0, abort, a.err));
     tc_fence_after();
 
     // Dual: slot 1 leaves its results in the buffers that only it has used (K's
@@ -644,9 +646,9 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
         else if (a.lse)
             a.lse[flat] = lse * kLog2ToNat;
     }
-    // Through the slot's Q buffer (every product with it is done), so that rows
-    // leave in whole lines: 16-byte pieces, swizzled by the row. fp32 partials
-    // take two passes of half the dims.
+    // Through the slot's Q buffer (all four warps have written it, every product
+    // with it is done), so that rows leave in whole lines: 16-byte pieces,
+    // swizzled by the row. fp32 partials take two passes of half the dims.
     uint8_t* stage = q + i * Tile<D>::BYTES;
     const bool partial = a.splits > 1;
     const int64_t own_at = !in ? -1 : partial ? part * D : tok * a.out.token_stride + (int64_t)qh * a.out.head_stride;
