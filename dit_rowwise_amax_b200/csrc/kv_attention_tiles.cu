@@ -621,19 +621,25 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
         if (*(volatile int*)&sm->failed[warp + 4]) ok = false;
     }
     if (!ok) return;
-    // out = (O x own + O' x theirs), O' of the other slot.
-    float own = 1.0f, theirs = 0.0f;
+    // out = (O own + O' theirs) 2^unit / l, O' of the other slot. The larger of
+    // the two slots' units 2^(m + v_ref) is the common one, so no factor exceeds
+    // one, whatever block scales either slot has met.
+    float own = 1.0f, theirs = 0.0f, unit = (float)v_ref;
     if (dual && w.n[1] > 0) {
         const float mo = meta[t], to = fmaxf(m, mo);
         if (to != kNegInf) {
-            const float x = ex2_approx(m - to), y = ex2_approx(mo - to);
+            const float x = ex2_approx(m - to), y = ex2_approx(mo - to), vo = meta[2 * kRows + t];
+            const float ahead = (m - mo) + ((float)v_ref - vo);
+            own = ex2_approx(fminf(ahead, 0.0f)), theirs = ex2_approx(fminf(-ahead, 0.0f));
+            unit = ahead >= 0.0f ? unit + (m - to) : vo + (mo - to);
             l = l * x + meta[kRows + t] * y;
-            own = x, theirs = y * ex2_approx(meta[2 * kRows + t] - (float)v_ref);
         }
         m = to;
     }
-    const float inv = l > 0.0f || l != l ? 1.0f / l * pow2f(v_ref) : 0.0f;
-    own *= inv, theirs *= inv;
+    // 2^unit may be 2^-120: half of it in front of the division, half behind.
+    const bool some = l > 0.0f || l != l;
+    const float half = some ? ex2_approx(0.5f * unit) : 0.0f, inv = some ? half / l : 0.0f;
+    own *= half, theirs *= half;
     // Taken again rather than kept in registers through the loop.
     const int token = in ? row / a.group : 0, qh = w.head * a.group + (in ? row % a.group : 0);
     const int64_t tok = w.r.first + token;
@@ -678,6 +684,8 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
                     y[4 * x + 3] = fmaf(z.w, theirs, y[4 * x + 3]);
                 }
             }
+#pragma unroll
+            for (int x = 0; x < 16; ++x) y[x] *= inv;
             auto put = [&](int piece, uint4 x) {
                 *reinterpret_cast<uint4*>(stage + t * (2 * D) + ((piece ^ (t & 7)) << 4)) = x;
             };

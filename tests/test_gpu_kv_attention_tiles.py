@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import attention_reference as ref
+from attention_bounds import attention_seen
 from test_gpu_kv_attention import filled
 from test_gpu_kv_cache import ints, offsets_of
 
@@ -345,4 +346,51 @@ def test_whole_video_over_itself():
     rows = torch.cat([torch.arange(0, n, 251), torch.tensor([127, 128, 255, 256, n - 1])])
     want, _, bound, _ = ref.attention(q[rows.cuda()], cache, [pages], [n], [0, len(rows)], dim ** -0.5, 0)
     assert bool(((out[rows.cuda()].double() - want).abs() <= bound).all())
+    assert fp8.device_error() == OK
+
+
+def check_seen(q, cache, pages, n, frame=0, scale=None, how="copies", **kw):
+    """One request against attention_bounds.attention_seen."""
+    scale = q.shape[2] ** -0.5 if scale is None else scale
+    copies, width = sizes_for_tiles(q.shape[1], cache, [pages], [n], [0, q.shape[0]], how)
+    got, lse = attend(q, cache, [pages], [n], [0, q.shape[0]], copies, width, frame, scale)
+    want, want_lse, bound, lse_bound = attention_seen(q, cache, pages, n, frame, scale, **kw)
+    err = (got.double() - want).abs()
+    assert bool((err <= bound).all()), f"worst error / bound {float((err / bound).max()):.3f}, NaN {bool(err.isnan().any())}"
+    fin = ~want_lse.isinf()
+    assert torch.equal(~fin, lse.isinf()) and bool(((lse.double() - want_lse).abs() <= lse_bound)[fin].all())
+
+
+@pytest.mark.parametrize("how", HOW)
+@pytest.mark.parametrize("small,large", [(-120, 9), (-120, 40), (-100, 30), (40, -100)])
+def test_slots_that_meet_value_scales_far_apart(small, large, how):
+    """At most 128 rows: the two slots take the even and the odd tiles of 128
+    keys, one of them with V far below the other's. First all rows see both,
+    then some see only the first tile: what the other holds is not theirs."""
+    g = torch.Generator("cuda").manual_seed(19)
+    new, heads, dim, t, n = 100, 1, 64, 128, 200
+    cache = filled(2, t, heads, dim, g)
+    cache.v_scale[0], cache.v_scale[1] = 2.0 ** small, 2.0 ** large
+    if small == -120:
+        cache.v[0] = 0
+    q = normal((new, heads, dim), g)
+    check_seen(q, cache, [0, 1], n, how=how)
+    check_seen(q, cache, [0, 1], n, 1, how=how)
+
+
+def test_smallest_values_over_a_long_cache():
+    """2^-112 on average over 12.6 million keys: 2^-120 over the softmax's sum
+    is far below fp32's normal range."""
+    requests, new, dim, t, n = 148, 20, 64, 128, 3 << 22
+    cache = filled(1, t, 1, dim, torch.Generator("cuda").manual_seed(20))
+    cache.v.fill_(0x78)  # 256
+    cache.v_scale.fill_(2.0 ** -120)
+    table = torch.zeros((requests, n // t), dtype=torch.int32, device="cuda")
+    q = torch.zeros((requests * new, 1, dim), dtype=torch.bfloat16, device="cuda")
+    args = (q, cache, table, ints([n] * requests), ints(offsets_of([new] * requests)))
+    assert fp8.kv_cache_attention_plan(*args, max_q=new) == (256, 1)
+    out, lse = fp8.kv_cache_attention(*args, max_q=new, return_lse=True)
+    # Equal weights and values: every sum of up to 2^24 of either is exact.
+    assert bool(((out.double() * 2.0 ** 112 - 1).abs() <= 2.0 ** -8 + 2.0 ** -20).all())
+    assert bool(((lse.double() - math.log(n)).abs() <= 2.0 ** -20 * math.log(n)).all())
     assert fp8.device_error() == OK
