@@ -153,6 +153,14 @@ __device__ __forceinline__ float pow2f(int n) { return __uint_as_float((uint32_t
 // log2 of a block's scale (a power of two).
 __device__ __forceinline__ int scale_log2_of(float s) { return (int)(__float_as_uint(s) >> 23) - 127; }
 
+// The softmax's references are lazy: they only move when a score exceeds them by
+// kLazy (log2 units). P goes into the product as 2^(kLift + score - reference),
+// at most 2^15 in fp16 (largest 65504), so that weights are normal numbers down
+// to 2^-21 of the reference's and count at all down to 2^-32: what a row of n
+// keys loses to the rounding of its small weights stays below n 2^-32 (without
+// the lift n 2^-25, 3% at a million keys).
+constexpr float kLazy = 8.0f, kLift = 7.0f;
+
 constexpr float kLog2ToNat = 0.6931471805599453f;
 
 #endif  // __CUDACC__

@@ -10,7 +10,7 @@
 //
 // Mathematics, per granule and warp (mma.sync m16n8k16, fp16 -> fp32):
 //     S^T = K Q^T      A = 16 keys x dim, B = 8 query rows per column tile
-//     P^T = 2^(t - m)  t = s + log2 S_V: the score plus V's block scale
+//     P^T = 2^(7 + t - m)  t = s + log2 S_V: the score plus V's block scale
 //     O^T += V^T P^T   A = dim x 16 keys, B = P^T
 // Keys and values are the A operands so that 8 rows fill a column tile (the
 // 16-row A side would be half empty at a group of 8 or fewer). Both products
@@ -24,13 +24,12 @@
 // The products are fp16 (attention.cuh says why; decoding to bf16 this kernel
 // issued 520 instructions per granule instead of 310 and was bound by them).
 // K's scale multiplies the score; V's is in the exponent of P, with a
-// reference m of its own, so P is exact to 2^-25 of the row's largest
+// reference m of its own, so P is exact to 2^-32 of the row's largest
 // contribution however V's scales differ. The softmax sum takes a second
 // exponential 2^(s - mu), in fp32.
 //
-// Both references are lazy: they only move when a score exceeds them by 8
-// (log2 units), so the usual granule needs one vote and no shuffles; p is at
-// most 2^8.
+// Both references are lazy (attention.cuh), so the usual granule needs one vote
+// and no shuffles.
 //
 // Bound: HBM, 2 bytes per token, kv head and dim. 32 requests of 100 .. 16001
 // tokens, 8 kv heads of 128, 4 query heads each: 103 us, 5.2 TB/s; alone and
@@ -46,7 +45,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kGranule = 16;
-constexpr float kLazy = 8.0f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -236,7 +234,7 @@ __device__ __forceinline__ void attend_granule(RowsState<D, NT>& st, const uint8
         for (int i = 0; i < 2; ++i) {
             // A row that has seen nothing yet has references of -inf; its scores are too.
             const float mu = st.mu[nt][i] == kNegInf ? 0.0f : st.mu[nt][i];
-            const float m = (st.m[nt][i] == kNegInf ? 0.0f : st.m[nt][i]) - ev;
+            const float m = (st.m[nt][i] == kNegInf ? 0.0f : st.m[nt][i]) - (ev + kLift);
             st.l[nt][i] += ex2_approx(s[nt][i] - mu) + ex2_approx(s[nt][i + 2] - mu);
             e[i] = ex2_approx(s[nt][i] - m);
             e[i + 2] = ex2_approx(s[nt][i + 2] - m);
@@ -419,9 +417,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3) kv_attn_rows(con
             const float4 y = *reinterpret_cast<const float4*>(&sm.o[w][q][d]);
             x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
         }
-        // out = x 2^(top - mu) / sum; the power in two steps, it may reach 2^-128.
+        // out = x 2^(top - kLift - mu) / sum; the power in two steps, it may reach 2^-128.
         const bool some = sum > 0.0f || sum != sum;
-        const float half = some ? ex2_approx(0.5f * (top - mu)) : 0.0f;
+        const float half = some ? ex2_approx(0.5f * (top - kLift - mu)) : 0.0f;
         const float inv = some ? half / sum : 0.0f;
         x.x = x.x * half * inv, x.y = x.y * half * inv, x.z = x.z * half * inv, x.w = x.w * half * inv;
         const int64_t token = r.first + row / a.group;

@@ -4,7 +4,7 @@
 // one kv head and one range of keys, and walks the range in tiles of 128 keys
 // with two slots, each 128 rows with a score tile S and an output O in TMEM:
 //     S = Q K^T        tcgen05.mma, Q and K in shared memory, S in TMEM
-//     P = 2^(c S - m)  a thread per row: TMEM -> registers -> fp16 -> TMEM
+//     P = 2^(7 + c S - m)  a thread per row: TMEM -> registers -> fp16 -> TMEM
 //     O += P V         tcgen05.mma, P from TMEM, V in shared memory, O in TMEM
 // one pass over the keys, with a running maximum and sum per row. With more
 // than 128 rows the slots are two row tiles that share every key tile; with
@@ -40,9 +40,8 @@
 // against 1.75): there the softmax's own time bounds it. Loads are far below
 // HBM.
 //
-// The running maximum is lazy: a row's reference moves, and O is rescaled,
-// only when a score exceeds it by 8 (log2 units), so after the first tiles O
-// stays in TMEM untouched by the softmax threads; p is at most 2^8.
+// The running maximum is lazy (attention.cuh), so after the first tiles O stays
+// in TMEM untouched by the softmax threads.
 //
 // Every wait is bounded; an expired one raises the error word and the CTA's
 // abort flag, lets copies and MMAs land, frees TMEM and returns. Warps that
@@ -56,7 +55,6 @@ namespace {
 constexpr int kRows = 128;  // rows of a slot = TMEM lanes
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kThreads = 512;
-constexpr float kLazy = 8.0f;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 // Registers per thread by role, out of the launch's 512 x 128. The softmax holds
@@ -483,7 +481,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
     const uint32_t lanes = (uint32_t)(t >> 5) << 21;  // this warp's TMEM lanes: (t / 32) * 32 << 16
     const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + 2 * kKeys + i * D;
     const int n = w.n[i];
-    float m = kNegInf, l = 0.0f;
+    float m = kNegInf, l = 0.0f;  // l in units of 2^(m - kLift), as P and O
     int v_ref = -120;  // O is in units of 2^v_ref
     bool ok = true;
     for (int j = 0; j < n; ++j) {
@@ -558,9 +556,9 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
                 }
             }
         }
-        const float neg = m == kNegInf ? 0.0f : -m;
+        const float neg = m == kNegInf ? 0.0f : kLift - m;
         const f32x2_t neg2 = f2_pack(neg, neg);
-        f32x2_t sum[2] = {f2_pack(l, 0.0f), f2_pack(0.0f, 0.0f)};
+        f32x2_t sum[2] = {f2_pack(0.0f, 0.0f), f2_pack(0.0f, 0.0f)};  // of this tile: small weights add up before they meet l
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -583,7 +581,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
             if (lane == 0) mbar_arrive(&sm->p_full[i][half]);
         }
         const float2 t2 = f2_unpack(f2_add(sum[0], sum[1]));
-        l = t2.x + t2.y;
+        l += t2.x + t2.y;
     }
     // The slot's O; without a key tile the slot's Q, whose buffer takes the rows
     // on their way out: every warp of the slot has to have written its own.
@@ -646,7 +644,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
     const int64_t flat = tok * a.q.heads + qh;
     const int64_t part = (int64_t)w.split * a.b.total * a.q.heads + flat;
     if (in) {
-        const float lse = m == kNegInf ? kNegInf : m + lg2_approx(l);
+        const float lse = m == kNegInf ? kNegInf : m - kLift + lg2_approx(l);
         if (a.splits > 1)
             a.part_lse[part] = lse;
         else if (a.lse)

@@ -502,7 +502,8 @@ fp8dit_status fp8_kv_cache_append(const fp8dit_kv_cache* cache, const fp8dit_hea
  * sees nothing is 0 (its lse -infinity). Scores, softmax sums and output are
  * held in fp32. Both products run in fp16, in which the codes are exact: q is
  * scaled by a power of two per row (what lies 2^-38 below the row's largest
- * |q| is lost), the block scales are applied outside, p is rounded to fp16.
+ * |q| is lost), the block scales are applied outside, p is rounded to fp16
+ * (what lies 2^-32 below the row's largest counts in the softmax's sum only).
  * With more than 16 rows (new tokens x query heads per kv head) a V block's
  * values below 2^-24 of the request's and head's largest block scale lose
  * bits, those of a block whose scale is below it count as 0. The output is

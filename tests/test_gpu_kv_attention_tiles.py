@@ -394,3 +394,34 @@ def test_smallest_values_over_a_long_cache():
     assert bool(((out.double() * 2.0 ** 112 - 1).abs() <= 2.0 ** -8 + 2.0 ** -20).all())
     assert bool(((lse.double() - math.log(n)).abs() <= 2.0 ** -20 * math.log(n)).all())
     assert fp8.device_error() == OK
+
+
+@pytest.mark.parametrize("requests,new,kernel", [(2400, 1, 8), (148, 200, 256)])
+def test_many_weights_far_below_the_largest(requests, new, kernel):
+    """A million keys at 2^-27 of one key's weight make up 2^-7 of the whole;
+    where that key's value is 0 they are all there is."""
+    dim, t, n = 64, 128, 1 << 20
+    cache = filled(2, t, 1, dim, torch.Generator("cuda").manual_seed(21))
+    cache.k_scale.fill_(1.0)
+    cache.v_scale.fill_(2.0 ** -8)
+    cache.k.zero_()
+    cache.k[:, :, :, 0] = 0xB8  # -1
+    cache.v.fill_(0x78)         # 256
+    cache.k[0, :, 0, 0] = 0     # the first block's first key: score 0, the others -27 (log2)
+    cache.v[0, :, 0, ::2] = 0
+    table = torch.ones((requests, n // t), dtype=torch.int32, device="cuda")
+    table[:, 0] = 0
+    q = torch.zeros((requests * new, 1, dim), dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 27.0
+    args = (q, cache, table, ints([n] * requests), ints(offsets_of([new] * requests)))
+    assert fp8.kv_cache_attention_plan(*args, max_q=new) == (kernel, 1)
+    out, lse = fp8.kv_cache_attention(*args, max_q=new, scale=math.log(2.0), return_lse=True)
+    mass = (n - 1) * 2.0 ** -27
+    # bf16 2^-8; a weight of 2^-20 is exact in fp16; the exponent -27 is off by
+    # 27 2^-23 or less (fp32 scale and product), exp2 by 2^-22, running fp32 sums of
+    # at most n / 64 terms by 2^-24 each.
+    near = 2.0 ** -8 + 27 * 2.0 ** -23 + 2.0 ** -22 + n / 64 * 2.0 ** -24
+    want = mass / (1 + mass)
+    assert bool(((out[:, :, ::2].double() - want).abs() <= near * want).all()), float(out[0, 0, 0]) / want
+    assert bool(((lse.double() - math.log1p(mass)).abs() <= n / 64 * 2.0 ** -24 + 2.0 ** -20).all())
+    assert fp8.device_error() == OK
