@@ -14,9 +14,16 @@
 //
 // The products are fp16 (attention.cuh says why). K's block scale multiplies
 // the scores; V is decoded as code x 2^(n - r), n its block's scale exponent
-// and r the largest one the CTA has met so far, so O is in units of 2^r and is
-// brought along when r grows. A V block is exact down to 2^-15 of the largest,
-// and better than P's own rounding down to 2^-24.
+// and r the largest one the CTA has met so far, so O is in units of 2^(m + r)
+// and is brought along when either grows. That is exact while n >= r - 14, and
+// r counts blocks that the mask hides from a row. So from the first tile on
+// after which the exponents met lie more than 14 apart, V is decoded as its
+// codes and n goes into P's exponent, with a reference per row for O's unit
+// from the keys that the row sees, and the softmax's sum takes a second
+// exponential ("wide" tiles, in a loop of their own: 2.4 times as long, 1560
+// rows x 16 heads over 32760 keys 1060 us instead of 444; 2^14 between two
+// blocks' largest values is rare). Blocks with the smallest scale 2^-120, which
+// blocks of zeros have, do not count for the distance.
 //
 // Warp roles (16 warps, one CTA per SM):
 //   0-3, 4-7   softmax of slot 0 and 1, a thread per row. P is handed over in
@@ -56,6 +63,8 @@ constexpr int kRows = 128;  // rows of a slot = TMEM lanes
 constexpr int kKeys = 128;  // keys of a tile
 constexpr int kThreads = 512;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kSpread = 14;      // exponents of V's scales that one unit covers exactly
+constexpr int kWide = 1000;  // in place of r: a wide tile
 
 // Registers per thread by role, out of the launch's 512 x 128. The softmax holds
 // a row's 128 scores: with 168 registers it spilled and was 6% slower, and with
@@ -82,8 +91,9 @@ struct Bars {
     uint64_t drain;
     alignas(16) float k_scale[kRing][kKeys / 16];  // of every 16 keys (read as float4)
     uint32_t bad[kRing];               // bad blocks, bit per block
-    int v_ref[kRing];                  // exponent r that V is decoded with
-    uint32_t v_mul[2][4];              // 2^(n - r) as fp16, twice: [half of the tile][block]; 0: V counts as 0
+    int v_ref[kRing];                // exponent r that V is decoded with, or kWide
+    float v_exp[kRing][kKeys / 16];    // n of every 16 keys
+    uint32_t v_mul[2][4];              // 2^(n - r) (wide: 1) as fp16, twice: [half of the tile][block]; 0: V counts as 0
     uint32_t tmem;
     int abort;
     int failed[8];  // softmax warp w saw an expired wait
@@ -168,7 +178,7 @@ __device__ __forceinline__ void load_role(const KvAttnArgs& a, Bars* sm, uint8_t
     };
     int page = fetch_page(), next = fetch_page();
     float sk = fetch_scale(a.c.ks, page), sv = fetch_scale(a.c.vs, page);
-    int v_ref = -120;
+    int v_ref = -120, v_low = 120;  // of the exponents met so far, all and those above -120
     // One raw stage: K's two halves, V's two halves.
     auto mine = [&](int st) { return T == 128 ? lane == 0 : lane < per_tile && ((lane << tlog) >> 6) == (st & 1); };
     const int key = (lane << tlog) & 63;  // first key of this lane's copy in its stage
@@ -188,11 +198,15 @@ __device__ __forceinline__ void load_role(const KvAttnArgs& a, Bars* sm, uint8_t
         const int after = fetch_page();
         const float nk = fetch_scale(a.c.ks, next), nv = fetch_scale(a.c.vs, next);
         const uint32_t bad = __ballot_sync(0xffffffffu, page == -2);
-        v_ref = max(v_ref, __reduce_max_sync(0xffffffffu, page >= 0 ? scale_log2_of(sv) : -120));
-        const int e = scale_log2_of(sv) - v_ref;
+        const int n = scale_log2_of(sv);
+        v_ref = max(v_ref, __reduce_max_sync(0xffffffffu, page >= 0 ? n : -120));
+        v_low = min(v_low, __reduce_min_sync(0xffffffffu, page >= 0 && n > -120 ? n : 120));
+        const bool wide = v_ref - v_low > kSpread;  // from here on: v_ref only grows, v_low only falls
+        const int e = wide ? 0 : n - v_ref;
         uint32_t mul = page < 0 || e < -24 ? 0u : e >= -14 ? (uint32_t)(15 + e) << 10 : 1u << (24 + e);
         mul |= mul << 16;
         const float sk16 = __shfl_sync(0xffffffffu, sk, (lane << 4 >> tlog) & 31);
+        const float n16 = __shfl_sync(0xffffffffu, (float)n, (lane << 4 >> tlog) & 31);
         bool fail = false;
         for (int st = 0; st < 4; ++st) {
             const int count = __popc(__ballot_sync(0xffffffffu, mine(st) && page >= 0));
@@ -206,10 +220,13 @@ __device__ __forceinline__ void load_role(const KvAttnArgs& a, Bars* sm, uint8_t
             }
             if (st >= 2 && mine(st)) sm->v_mul[st & 1][key >> tlog] = mul;
             if (st == 0) {
-                if (lane < kKeys / 16) sm->k_scale[g % kRing][lane] = sk16;
+                if (lane < kKeys / 16) {
+                    sm->k_scale[g % kRing][lane] = sk16;
+                    sm->v_exp[g % kRing][lane] = n16;
+                }
                 if (lane == 0) {
                     sm->bad[g % kRing] = bad;
-                    sm->v_ref[g % kRing] = v_ref;
+                    sm->v_ref[g % kRing] = wide ? kWide : v_ref;
                     if (bad) atomicOr(a.err.word, kDevErrIndex);
                 }
             }
@@ -418,6 +435,83 @@ __device__ __forceinline__ void mma_role(const KvAttnArgs& a, Bars* sm, const ui
 }
 
 // --------------------------------------------------------------- softmax
+// This warp's 32 rows of O times a factor per row.
+template <int D>
+__device__ __forceinline__ void scale_rows(uint32_t o_addr, float by) {
+#pragma unroll 1
+    for (int k = 0; k < D / 16; ++k) {
+        uint32_t o[16];
+        tmem_ld_32x32b_x16(o_addr + 16 * k, o);
+        tmem_wait_ld16(o);
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * by);
+        tmem_st_32x32b_x16(o_addr + 16 * k, o);
+    }
+}
+
+// A wide tile of slot i, 16 keys at a time: the scores are read from TMEM once
+// for the references and once for the weights, and a chunk's P goes into
+// columns whose scores have been read. Keys from `seen` on and bad blocks are
+// masked. O's unit 2^u, u = m + v_ref, follows the largest score plus exponent
+// that the row has seen; the first time u is what the tiles before used, which
+// may lie kSpread + 1 above that.
+template <int D>
+__device__ __forceinline__ void wide_tile(Bars* sm, int i, int ring, int block_log2, uint32_t s_addr, uint32_t o_addr, float c,
+                                          int seen, uint32_t bad, bool have_o, bool first, int lane, float& m, float& l,
+                                          float& v_ref) {
+    const float *ks = sm->k_scale[ring], *vn = sm->v_exp[ring];
+    uint32_t s[16];
+    auto scores = [&](int k) {
+        tmem_ld_32x32b_x16(s_addr + 16 * k, s);
+        tmem_wait_ld16(s);
+        const int end = bad >> (16 * k >> block_log2) & 1u ? 0 : seen - 16 * k;
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+            if (x >= end) s[x] = __float_as_uint(kNegInf);
+        return fmaxf(c * ks[k], 0x1p-126f);
+    };
+    float top = kNegInf, most = kNegInf;
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+        const float f = scores(k);
+        float t = __uint_as_float(s[0]);
+#pragma unroll
+        for (int x = 1; x < 16; ++x) t = fmaxf(t, __uint_as_float(s[x]));
+        top = fmaxf(top, t * f);
+        most = fmaxf(most, t * f + vn[k]);
+    }
+    const float to = fmaxf(m, ceilf(top)), was = m + v_ref;
+    const float u = fmaxf(first ? was - (kSpread + 1) : was, ceilf(most));
+    const bool any = to != kNegInf;  // else the row has seen nothing yet: O is 0
+    if (have_o) scale_rows<D>(o_addr, any ? ex2_approx(was - u) : 1.0f);
+    const float lift = any ? kLift - to : 0.0f, lift_u = any ? kLift - u : 0.0f;
+    if (any) {
+        l *= ex2_approx(m - to);
+        v_ref = u - to;
+        m = to;
+    }
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+        const float f = scores(k), e = lift_u + vn[k];
+        float sum = 0.0f;
+        uint32_t p[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const float s0 = __uint_as_float(s[2 * x]), s1 = __uint_as_float(s[2 * x + 1]);
+            sum += ex2_approx(fmaf(s0, f, lift)) + ex2_approx(fmaf(s1, f, lift));
+            p[x] = pack_f16x2(ex2_approx(fmaf(s0, f, e)), ex2_approx(fmaf(s1, f, e)));
+        }
+        tmem_st_32x32b_x8(s_addr + 8 * k, p);
+        l += sum;
+        if ((k & 3) == 3) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm->p_full[i][k >> 2]);
+        }
+    }
+}
+
 // Thread t of 128: a row of slot i.
 template <int D>
 __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint8_t* q, uint8_t* tiles, uint32_t tmem,
@@ -481,10 +575,13 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
     const uint32_t lanes = (uint32_t)(t >> 5) << 21;  // this warp's TMEM lanes: (t / 32) * 32 << 16
     const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + 2 * kKeys + i * D;
     const int n = w.n[i];
-    float m = kNegInf, l = 0.0f;  // l in units of 2^(m - kLift), as P and O
-    int v_ref = -120;  // O is in units of 2^v_ref
+    // m is a whole number (or -inf), so units change by powers of two. P and l are
+    // in units of 2^(m - kLift), O in units of 2^(m - kLift + r_now).
+    float m = kNegInf, l = 0.0f;
+    int r_now = -120;
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
+    int j = 0;
+    for (; j < n; ++j) {
         const int g = dual ? 2 * j + i : j;
         ok = __all_sync(0xffffffffu, wait_for(&sm->s_full[i], (uint32_t)j & 1u, abort, a.err));
         if (!ok) break;
@@ -537,24 +634,15 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
             u0 = max3(u0, __uint_as_float(y[14]), __uint_as_float(y[15]));
             tile_top = fmaxf(tile_top, fmaxf(u0, u1) * f[z]);
         }
-        if (__builtin_expect(__any_sync(0xffffffffu, tile_top > m + kLazy) || r != v_ref, 0)) {
-            const float to = fmaxf(m, tile_top);
+        if (__builtin_expect(__any_sync(0xffffffffu, tile_top > m + kLazy) || r != r_now, 0)) {
+            if (r == kWide) break;  // and so are all tiles behind it
+            const float to = fmaxf(m, ceilf(tile_top));
             const float down = to == kNegInf ? 1.0f : ex2_approx(m - to);
-            const float fo = down * ex2_approx((float)(v_ref - r));
+            const float fo = down * ex2_approx((float)(r_now - r));
             m = to;
             l *= down;
-            v_ref = r;
-            if (j > 0) {  // O of the earlier tiles is complete: S came after it
-#pragma unroll 1
-                for (int k = 0; k < D / 16; ++k) {
-                    uint32_t o[16];
-                    tmem_ld_32x32b_x16(o_addr + 16 * k, o);
-                    tmem_wait_ld16(o);
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * fo);
-                    tmem_st_32x32b_x16(o_addr + 16 * k, o);
-                }
-            }
+            r_now = r;
+            if (j > 0) scale_rows<D>(o_addr, fo);  // O of the earlier tiles is complete: S came after it
         }
         const float neg = m == kNegInf ? 0.0f : kLift - m;
         const f32x2_t neg2 = f2_pack(neg, neg);
@@ -583,6 +671,15 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
         const float2 t2 = f2_unpack(f2_add(sum[0], sum[1]));
         l += t2.x + t2.y;
     }
+    float v_ref = (float)r_now;  // from here on any number, in place of r_now
+    for (bool first = true; ok && j < n; ++j, first = false) {
+        const int g = dual ? 2 * j + i : j;
+        ok = __all_sync(0xffffffffu, wait_for(&sm->s_full[i], (uint32_t)j & 1u, abort, a.err));
+        if (!ok) break;
+        tc_fence_after();
+        wide_tile<D>(sm, i, g % kRing, a.c.block_log2, s_addr, o_addr, c, limit - g * kKeys,
+                     *(volatile uint32_t*)&sm->bad[g % kRing], j > 0, first, lane, m, l, v_ref);
+    }
     // The slot's O; without a key tile the slot's Q, whose buffer takes the rows
     // on their way out: every warp of the slot has to have written its own.
     if (ok) ok = __all_sync(0xffffffffu, wait_for(n > 0 ? &sm->o_full[i] : &sm->q_full[dual ? 0 : i], 0, abort, a.err));
@@ -599,7 +696,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
         if (i == 1 && ok) {
             meta[t] = m;
             meta[kRows + t] = l;
-            meta[2 * kRows + t] = (float)v_ref;
+            meta[2 * kRows + t] = v_ref;
             if (n > 0) {
 #pragma unroll 1
                 for (int k = 0; k < D / 16; ++k) {
@@ -622,12 +719,12 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
     // out = (O own + O' theirs) 2^unit / l, O' of the other slot. The larger of
     // the two slots' units 2^(m + v_ref) is the common one, so no factor exceeds
     // one, whatever block scales either slot has met.
-    float own = 1.0f, theirs = 0.0f, unit = (float)v_ref;
+    float own = 1.0f, theirs = 0.0f, unit = v_ref;
     if (dual && w.n[1] > 0) {
         const float mo = meta[t], to = fmaxf(m, mo);
         if (to != kNegInf) {
             const float x = ex2_approx(m - to), y = ex2_approx(mo - to), vo = meta[2 * kRows + t];
-            const float ahead = (m - mo) + ((float)v_ref - vo);
+            const float ahead = (m - mo) + (v_ref - vo);
             own = ex2_approx(fminf(ahead, 0.0f)), theirs = ex2_approx(fminf(-ahead, 0.0f));
             unit = ahead >= 0.0f ? unit + (m - to) : vo + (mo - to);
             l = l * x + meta[kRows + t] * y;

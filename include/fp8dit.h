@@ -504,10 +504,9 @@ fp8dit_status fp8_kv_cache_append(const fp8dit_kv_cache* cache, const fp8dit_hea
  * scaled by a power of two per row (what lies 2^-38 below the row's largest
  * |q| is lost), the block scales are applied outside, p is rounded to fp16
  * (what lies 2^-32 below the row's largest counts in the softmax's sum only).
- * With more than 16 rows (new tokens x query heads per kv head) a V block's
- * values below 2^-24 of the request's and head's largest block scale lose
- * bits, those of a block whose scale is below it count as 0. The output is
- * rounded once to bf16.
+ * Blocks whose |v| are all at most 448 2^-120 (their scale is the smallest)
+ * lose bits beside blocks whose scale is above 2^-106, and count as zeros above
+ * 2^-96. The output is rounded once to bf16.
  *   cache      no NaN codes or scales among a request's kv_lens[b] tokens; what lies behind them does not matter.
  *   q, out     bf16 [total_tokens, q heads, head_dim]; q.heads % kv_heads == 0; q finite;
  *              out must not overlap the inputs.

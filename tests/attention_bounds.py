@@ -8,7 +8,7 @@ import torch
 import attention_reference as ref
 
 
-def attention_seen(q, cache, pages, n, frame, scale, by_contribution=False):
+def attention_seen(q, cache, pages, n, frame, scale, floor="weight"):
     """(out, lse, bound, lse_bound) of one request, q [new, heads, dim], its
     last tokens being the queries.
 
@@ -18,8 +18,9 @@ def attention_seen(q, cache, pages, n, frame, scale, by_contribution=False):
     on top). So the floor is 2^-31 sum_t r_t 448 S_t, r_t the running maximum
     of p over the keys up to the end of t's 128 keys (a later, larger p scales
     the earlier error down with it), S_t the block's scale, which carries codes
-    up to 448. Where the block scale is part of p's exponent (by_contribution)
-    r_t S_t is the running maximum of p S instead.
+    up to 448. Where the block scale is part of p's exponent (floor =
+    "contribution") the running maximum of p S takes the place of r_t S_t;
+    "either": whichever is larger, for calls that do both.
     A score is an fp32 sum of D products: off by at most (D + 4) 2^-24 scale
     sum |q k| plus D 2^-38 scale max |q| max |k| (q's own scaling); exp2 adds
     2^-22 and its argument's rounding, 2^-24 of the distance to the reference
@@ -48,8 +49,9 @@ def attention_seen(q, cache, pages, n, frame, scale, by_contribution=False):
         mass, top, expo = most(x.abs() @ kk.abs().T * scale), most(s.abs()), most(sv.log2().abs()[None].expand_as(s))
         e = (dim + 4) * 2.0 ** -24 * mass + 2.0 ** -22 + 2.0 ** -24 * (2 * 1.45 * top + expo)
         e = e + dim * 2.0 ** -38 * scale * x.abs().amax(1) * most(kk.abs().amax(1)[None].expand_as(s))
-        run = (torch.cummax(p * sv, 1).values[:, ends] if by_contribution else torch.cummax(p, 1).values[:, ends] * sv)
-        floor = 2.0 ** -31 * 448 * torch.where(seen, run, torch.zeros_like(s)).sum(1)
-        bound = 1.01 * (2.0 ** -11 * a + 2.0 ** -8 * out.abs()) + (2 * e + 2 * n * 2.0 ** -24)[:, None] * a + floor[:, None] + 1e-44
+        weight, contribution = torch.cummax(p, 1).values[:, ends] * sv, torch.cummax(p * sv, 1).values[:, ends]
+        run = {"weight": weight, "contribution": contribution, "either": torch.maximum(weight, contribution)}[floor]
+        lost = 2.0 ** -31 * 448 * torch.where(seen, run, torch.zeros_like(s)).sum(1)
+        bound = 1.01 * (2.0 ** -11 * a + 2.0 ** -8 * out.abs()) + (2 * e + 2 * n * 2.0 ** -24)[:, None] * a + lost[:, None] + 1e-44
         outs.append((out, z, bound, e + n * 2.0 ** -24 + 2.0 ** -22 * (1 + z.abs().nan_to_num(posinf=0.0))))
     return [torch.stack(y, 1) for y in zip(*outs)]

@@ -425,3 +425,58 @@ def test_many_weights_far_below_the_largest(requests, new, kernel):
     assert bool(((out[:, :, ::2].double() - want).abs() <= near * want).all()), float(out[0, 0, 0]) / want
     assert bool(((lse.double() - math.log1p(mass)).abs() <= n / 64 * 2.0 ** -24 + 2.0 ** -20).all())
     assert fp8.device_error() == OK
+
+
+@pytest.mark.parametrize("new", [150, 300])
+@pytest.mark.parametrize("apart", [25, 60, 200])
+def test_blocks_that_the_mask_hides_do_not_count(new, apart):
+    """The first rows see only blocks with V far below that of the blocks that
+    the mask hides from them, some in the same 128 keys."""
+    g = torch.Generator("cuda").manual_seed(22)
+    heads, dim, t, n = 2, 64, 16, 330
+    cache = filled(21, t, 1, dim, g)
+    cache.v_scale.fill_(2.0 ** (100 - apart))
+    cache.v_scale[7::3] = 2.0 ** 100
+    check_seen(normal((new, heads, dim), g), cache, list(range(21)), n, 1, floor="contribution")
+
+
+@pytest.mark.parametrize("how", HOW)
+@pytest.mark.parametrize("new", [60, 300])
+@pytest.mark.parametrize("apart", [20, 35, 90])
+def test_rows_whose_weight_lies_on_a_small_block(new, apart, how):
+    """One block's scores are 2^45 above the others', its V 2^apart below
+    theirs: with 20 and 35 it still makes up the row."""
+    g = torch.Generator("cuda").manual_seed(23)
+    heads, dim, t, n = 1, 128, 32, 600
+    cache = filled(19, t, heads, dim, g)
+    cache.v_scale[6] = 2.0 ** (-8 - apart)
+    q = normal((new, heads, dim), g)
+    q[:, :, 0] = 4.0
+    cache.k[:, :, :, 0] = 0
+    cache.k_scale.fill_(2.0 ** -9)
+    cache.k[6, :, :, 0] = 0x7E  # 448 2^-9 x 4 = 3.5
+    scale = 45 * math.log(2.0) / 3.5
+    cache.k[:, :, :, 1:] = cache.k[:, :, :, 1:] & 0x9F  # other products small beside that
+    check_seen(q, cache, list(range(19)), n, scale=scale, how=how, floor="either" if how == "loose" else "contribution")
+
+
+@pytest.mark.parametrize("how", HOW)
+@pytest.mark.parametrize("new,frame", [(40, 0), (128, 1), (300, 0), (300, 7)])
+@pytest.mark.parametrize("dim,t", [(64, 16), (128, 32), (64, 128)])
+def test_value_scales_anywhere(new, frame, dim, t, how):
+    """Tiles with one unit first, then blocks whose V scales go up and down by
+    anything up to 2^200, zeros and bad blocks among them."""
+    g = torch.Generator("cuda").manual_seed(24)
+    heads, n = 2, 11 * 128 - 3
+    blocks = 11 * 128 // t
+    cache = filled(blocks, t, 1, dim, g)
+    e = torch.randint(-100, 100, (blocks,), generator=torch.Generator().manual_seed(new + dim))
+    e[: 3 * 128 // t] = e[: 3 * 128 // t] % 12
+    e[blocks // 2] = -120
+    cache.v[blocks // 2] = 0
+    cache.v_scale.copy_(torch.exp2(e.float())[:, None])
+    pages = list(range(blocks))
+    check_seen(normal((new, heads, dim), g), cache, pages, n, frame, how=how, floor="either")
+    cache.v[blocks - 2], cache.k[blocks - 2] = 0xFF, 0x7F  # what a bad index may not reach
+    check(normal((new, heads, dim), g), cache, [pages[: blocks - 2] + [-1, blocks - 1]], [n], [0, new], frame, how=how)
+    assert fp8.device_error() == INDEX
