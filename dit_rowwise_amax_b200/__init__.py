@@ -727,7 +727,9 @@ def _kv_batch(block_table: torch.Tensor, kv_lens: torch.Tensor, offsets: torch.T
         max_kv = min(width * block_tokens, 1 << 30)
     if not (0 <= max_new < 1 << 31 and 0 <= max_kv < 1 << 31):  # ctypes would cut them to 32 bits
         raise ValueError("the bounds of a request's new and cached tokens must be in 0 .. 2^31 - 1")
-    return _KvBatch(block_table.data_ptr(), kv_lens.data_ptr(), offsets.data_ptr(), total, n, width, max_new, max_kv)
+    # A bound of 0 would make the library's call a no-op that looks at nothing;
+    # with 1 it checks every request's numbers, and one without new tokens is skipped.
+    return _KvBatch(block_table.data_ptr(), kv_lens.data_ptr(), offsets.data_ptr(), total, n, width, max(max_new, 1), max_kv)
 
 
 def kv_cache_append(cache: Union[KVCache, Sequence[torch.Tensor]], k: torch.Tensor, v: torch.Tensor,
@@ -740,7 +742,8 @@ def kv_cache_append(cache: Union[KVCache, Sequence[torch.Tensor]], k: torch.Tens
     // block tokens]. A block's scale grows with its tokens, its older codes
     are brought along. block_table, kv_lens, offsets: int32 on the device
     (a captured graph reads their values at each replay); max_new bounds the
-    new tokens of one request. A block may be written by one request only.
+    new tokens of one request (0 counts as 1). A block may be written by one
+    request only, and stands once in its table.
     Rows past offsets[-1] are not read. Numbers outside their range are
     skipped and reported by device_error() (INDEX).
     """
@@ -765,7 +768,9 @@ def kv_cache_attention(q: torch.Tensor, cache: Union[KVCache, Sequence[torch.Ten
     tokens; causal = g: it sees the frames of g tokens up to its own whole
     (1: the usual causal mask), the queries being the last tokens. A row that
     sees nothing is 0. Returns out, or (out, lse) with the float32 [total,
-    heads] natural log-sum-exp. Rows past offsets[-1] are left as they are.
+    heads] natural log-sum-exp. Rows past offsets[-1], and those of a request
+    that device_error() reports, are left as they are: whatever the memory held
+    in tensors that are allocated here.
     workspace: device scratch for split key ranges, allocated here if absent
     (calls that overlap on the GPU must not share one).
     """

@@ -465,7 +465,9 @@ typedef struct {
  *   max_kv       bound of kv_lens[b], at most table_width * block_tokens.
  * A request whose numbers break these bounds is left out, and so is a token
  * whose block index is not in 0 .. n_blocks - 1 (attention sees it as masked);
- * both raise FP8DIT_ERR_INDEX in fp8dit_device_error().
+ * both raise FP8DIT_ERR_INDEX in fp8dit_device_error(). A call with n_requests,
+ * total_tokens or max_new 0 returns FP8DIT_OK and does nothing: the device
+ * arrays are not read, so nothing is reported either.
  */
 typedef struct {
     const int32_t* block_table;
@@ -487,7 +489,8 @@ typedef struct {
  * brought to the new scale, and the new codes are RNEsat(x / S). Blocks that
  * are not reached keep every bit.
  *   k, v  bf16 [total_tokens, kv_heads, head_dim]; finite values.
- * A block may be written by one request only (several may read it).
+ * A block may be written by one request only (several may read it) and stands
+ * once in its table.
  */
 fp8dit_status fp8_kv_cache_append(const fp8dit_kv_cache* cache, const fp8dit_heads* k, const fp8dit_heads* v,
                                   const fp8dit_kv_batch* batch, fp8dit_stream_t stream);
