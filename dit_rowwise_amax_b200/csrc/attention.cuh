@@ -60,6 +60,7 @@ struct KvAttnArgs {
     HeadsView q, out;
     float* lse;         // [total, q heads] or null
     float scale_log2;   // softmax scale * log2(e)
+    int32_t q_most;     // bound of q's exponent: scale_log2 / 2^q_most is a normal number
     int32_t group;      // query heads per kv head
     int32_t frame;      // causal granularity, 0: none
     int32_t splits;     // key ranges per (row tile, kv head)
@@ -144,11 +145,16 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 // is exact there and decoding is one instruction for two codes (four to bf16).
 // q is brought to [2^14, 2^15) by a power of two per row (q_exponent, from the
 // row's largest |q|), undone in the score; what lies 2^-38 below the row's
-// largest is lost, as in any fp32 sum of products (the exponent's bounds: the
-// largest bf16 still comes below 2^15, rows below 2^-105 keep 2^119).
-__device__ __forceinline__ int q_exponent(uint32_t amax_bf16_bits) {
-    return max(-113, min(119, 14 + 127 - (int)(amax_bf16_bits >> 7)));
+// largest is lost, as in any fp32 sum of products. The exponent's bounds: the
+// largest bf16 still comes below 2^15, rows below 2^-105 keep 2^119, or less
+// (KvAttnArgs::q_most) where the softmax scale over it would not be a normal
+// number: such rows' scores are then below 2^-5.
+__device__ __forceinline__ int q_exponent(uint32_t amax_bf16_bits, int most) {
+    return max(-113, min(most, 14 + 127 - (int)(amax_bf16_bits >> 7)));
 }
+// A score's factor: softmax scale over q's, times K's block scale. Not 0, so a
+// masked score of -inf stays one; not infinite, so a product of 0 stays 0.
+__device__ __forceinline__ float score_factor(float c, float k_scale) { return fminf(fmaxf(c * k_scale, 0x1p-126f), 0x1.fp127f); }
 __device__ __forceinline__ float pow2f(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }  // -126 .. 127
 // log2 of a block's scale (a power of two).
 __device__ __forceinline__ int scale_log2_of(float s) { return (int)(__float_as_uint(s) >> 23) - 127; }

@@ -2,6 +2,7 @@
 // include/fp8dit.h): rotary positions, the key / value cache's append and
 // attention over it. Arguments are checked here; nothing is computed on the
 // host but the launch's size and the rotary frequencies in turns.
+#include <algorithm>
 #include <cmath>
 
 #include "attention.cuh"
@@ -187,7 +188,8 @@ fp8dit_status fp8_kv_cache_attention(const fp8dit_kv_cache* cache, const fp8dit_
     if (q->heads <= 0 || q->heads % a.c.heads != 0) return invalid("q's heads must be a multiple of the cache's");
     if (q->heads > kMaxHeads) return unsupported("too many query heads");
     if (out->heads != q->heads) return invalid("out's heads differ from q's");
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return invalid("scale must be finite and > 0");
+    const float scale_log2 = scale * 1.4426950408889634f;
+    if (!(scale > 0.0f) || !std::isfinite(scale_log2)) return invalid("scale must be > 0 and finite, times log2(e) too");
     if (causal < 0) return invalid("causal must be >= 0");
     if (nothing(a.b)) return FP8DIT_OK;
     for (const fp8dit_heads* x : {q, out})
@@ -207,7 +209,8 @@ fp8dit_status fp8_kv_cache_attention(const fp8dit_kv_cache* cache, const fp8dit_
     }
     a.q = view(*q), a.out = view(*out);
     a.lse = lse;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = scale_log2;
+    a.q_most = std::min(119, 126 + std::ilogb(scale_log2));
     a.group = q->heads / a.c.heads;
     a.frame = causal;
     a.err = DevErr{dev->err_word, kDefaultWaitLimitNs};

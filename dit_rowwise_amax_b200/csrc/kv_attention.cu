@@ -178,7 +178,7 @@ __device__ __forceinline__ void attend_granule(RowsState<D, NT>& st, const uint8
     bool over = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const float f0 = st.cq[nt][0] * ks, f1 = st.cq[nt][1] * ks;
+        const float f0 = score_factor(st.cq[nt][0], ks), f1 = score_factor(st.cq[nt][1], ks);
 #pragma unroll
         for (int i = 0; i < 4; ++i) s[nt][i] *= i & 1 ? f1 : f0;
     }
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3) kv_attn_rows(con
         top = fold_halves(top);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = q_exponent(top);
+        const int e = q_exponent(top, a.q_most);
         const float f = pow2f(e), back = pow2f(-e);
 #pragma unroll
         for (int s = 0; s < D / 16; ++s)

@@ -468,7 +468,7 @@ __device__ __forceinline__ void wide_tile(Bars* sm, int i, int ring, int block_l
 #pragma unroll
         for (int x = 0; x < 16; ++x)
             if (x >= end) s[x] = __float_as_uint(kNegInf);
-        return fmaxf(c * ks[k], 0x1p-126f);
+        return score_factor(c, ks[k]);
     };
     float top = kNegInf, most = kNegInf;
 #pragma unroll 1
@@ -553,11 +553,11 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
             const uint32_t x = __shfl_sync(0xffffffffu, top[k], (lane % kAtOnce) * kLanes);
             if (lane / kAtOnce == k) mine = x;
         }
-        c = a.scale_log2 * pow2f(-q_exponent(mine));
+        c = a.scale_log2 * pow2f(-q_exponent(mine, a.q_most));
         if (!dual || i == 0) {
 #pragma unroll
             for (int k = 0; k < kLanes; ++k) {
-                const float f = pow2f(q_exponent(top[k]));
+                const float f = pow2f(q_exponent(top[k], a.q_most));
                 const int r = (t & 96) + k * kAtOnce + lane / kLanes;
                 uint32_t* y = &v[k].x;
 #pragma unroll
@@ -589,12 +589,12 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
         uint32_t s[4][32];
 #pragma unroll
         for (int k = 0; k < 4; ++k) tmem_ld_32x32b_x32(s_addr + 32 * k, s[k]);
-        float f[8];  // score factors of 16 keys each; not 0: a masked score of -inf stays one
+        float f[8];  // score factors of 16 keys each
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             const float4 ks = *reinterpret_cast<const float4*>(&sm->k_scale[g % kRing][4 * k]);
-            f[4 * k] = fmaxf(c * ks.x, 0x1p-126f), f[4 * k + 1] = fmaxf(c * ks.y, 0x1p-126f);
-            f[4 * k + 2] = fmaxf(c * ks.z, 0x1p-126f), f[4 * k + 3] = fmaxf(c * ks.w, 0x1p-126f);
+            f[4 * k] = score_factor(c, ks.x), f[4 * k + 1] = score_factor(c, ks.y);
+            f[4 * k + 2] = score_factor(c, ks.z), f[4 * k + 3] = score_factor(c, ks.w);
         }
         const int seen = limit - g * kKeys;  // this row sees columns below it
         const uint32_t bad = *(volatile uint32_t*)&sm->bad[g % kRing];

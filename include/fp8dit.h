@@ -514,7 +514,7 @@ fp8dit_status fp8_kv_cache_append(const fp8dit_kv_cache* cache, const fp8dit_hea
  *   q, out     bf16 [total_tokens, q heads, head_dim]; q.heads % kv_heads == 0; q finite;
  *              out must not overlap the inputs.
  *   lse        fp32 [total_tokens, q heads], contiguous: natural log of the sum of exp(scale q . K_t); or NULL.
- *   scale      finite, > 0.
+ *   scale      > 0, and finite times log2(e); scores scale q . K_t have to be within fp32's range.
  *   workspace  DEVICE scratch of at least fp8_kv_cache_attention_workspace_size(...) bytes, 16-byte aligned
  *              (may be NULL when that is 0); its contents do not matter, calls that overlap must not share it.
  * Few queries over many tokens: the tokens are split over CTAs and their
