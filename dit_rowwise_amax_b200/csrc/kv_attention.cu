@@ -46,6 +46,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kGranule = 16;
 constexpr float kNegInf = -__builtin_huge_valf();
+constexpr int kMostRanges = 64;  // of keys, that a call is cut into
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                           uint32_t b1) {
@@ -451,20 +452,27 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
     const int64_t flat = (int64_t)r.first * a.q.heads + row;
     const int64_t stride = (int64_t)a.b.total * a.q.heads;
     const int n = max(1, (r.len + a.chunk - 1) / a.chunk);  // splits that hold keys of this request
-    float top = kNegInf;
-    for (int i = lane; i < n; i += 32) top = fmaxf(top, a.part_lse[i * stride + flat]);
+    // Lane l has the weights of ranges l and l + 32, brought to a sum of one
+    // before they meet the ranges' rows: no term is larger than the result may be.
+    static_assert(kMostRanges <= 64, "two ranges per lane");
+    const float e0 = lane < n ? a.part_lse[lane * stride + flat] : kNegInf;
+    const float e1 = lane + 32 < n ? a.part_lse[(lane + 32) * stride + flat] : kNegInf;
+    float top = fmaxf(e0, e1);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+    float w0 = e0 == kNegInf ? 0.0f : ex2_approx(e0 - top), w1 = e1 == kNegInf ? 0.0f : ex2_approx(e1 - top);
+    float sum = w0 + w1;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);
+    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
+    w0 *= inv, w1 *= inv;
     constexpr int V = D / 32;  // outputs per lane
-    float x[V], sum = 0.0f;
+    float x[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) x[j] = 0.0f;
 #pragma unroll 4
     for (int i = 0; i < n; ++i) {
-        const float lse = a.part_lse[i * stride + flat];
-        if (lse == kNegInf) continue;
-        const float w = ex2_approx(lse - top);
-        sum += w;
+        const float w = __shfl_sync(0xffffffffu, i < 32 ? w0 : w1, i & 31);
         const float* p = a.part_o + (i * stride + flat) * D + lane * V;
         float y[V];
         if (V == 4)
@@ -472,14 +480,13 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
         else
             *reinterpret_cast<float2*>(y) = *reinterpret_cast<const float2*>(p);
 #pragma unroll
-        for (int j = 0; j < V; ++j) x[j] += w * y[j];
+        for (int j = 0; j < V; ++j) x[j] += w == 0.0f ? 0.0f : w * y[j];
     }
-    const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
     const int64_t token = r.first + row / a.q.heads;
     const int qh = (int)(row % a.q.heads);
     uint16_t* dst = a.out.ptr + token * a.out.token_stride + (int64_t)qh * a.out.head_stride + lane * V;
 #pragma unroll
-    for (int j = 0; j < V; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack_bf16x2(x[j] * inv, x[j + 1] * inv);
+    for (int j = 0; j < V; j += 2) *reinterpret_cast<uint32_t*>(dst + j) = pack_bf16x2(x[j], x[j + 1]);
     if (lane == 0 && a.lse) a.lse[flat] = top == kNegInf ? kNegInf : kLog2ToNat * (top + lg2_approx(sum));
 }
 
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
 // 0.6% slower on average, 21% at most.
 // Then the keys are cut into ranges whose results kv_attn_join joins:
 //  - kv_attn_rows: until four CTAs run on every SM (one wave), with ranges of
-//    at least 256 keys and at most 64 of them; beyond one wave, ranges of
+//    at least 256 keys and at most kMostRanges of them; beyond one wave, ranges of
 //    about 1024 keys while they are at most 16 CTAs per SM, which even out
 //    requests of different lengths. 16 heads over 1000 tokens take 8.3 us in 4
 //    ranges and 10.8 in 2; 32 x 8 over 4000 50.9 us in 4 ranges, 53.4 in 8 and
@@ -542,7 +549,7 @@ KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads,
         const bool tail = rem > 0 && rem <= 128;
         const int64_t full = heads * (p.row_tiles - (tail ? 1 : 0)), small = tail ? heads : 0;
         const double kv_tiles = (double)((kv + 127) / 128), row_bytes = (double)b.total * q_heads * (c.dim + 1) * 4.0;
-        most = std::min<int64_t>((kv + 511) / 512, 32);
+        most = std::min<int64_t>((kv + 511) / 512, kMostRanges / 2);
         double best = tensor_cost(full, small, kv_tiles, row_bytes, 1, num_sms);
         for (int64_t s = 2; s <= most; ++s) {
             const double cost = tensor_cost(full, small, kv_tiles, row_bytes, s, num_sms);
@@ -555,7 +562,7 @@ KvAttnPlan kv_attn_plan(const KvCacheView& c, const KvBatchView& b, int q_heads,
     } else {
         const int64_t even = std::min<int64_t>((16ll * num_sms + ctas - 1) / ctas, (kv + 1023) / 1024);
         splits = std::max<int64_t>(4ll * num_sms / ctas, even);
-        most = std::min<int64_t>((kv + 255) / 256, 64);
+        most = std::min<int64_t>((kv + 255) / 256, kMostRanges);
     }
     splits = std::max<int64_t>(1, std::min(splits, most));
     int64_t chunk = (b.max_kv + splits - 1) / splits;
