@@ -452,13 +452,13 @@ __device__ __forceinline__ void scale_rows(uint32_t o_addr, float by) {
 // A wide tile of slot i, 16 keys at a time: the scores are read from TMEM once
 // for the references and once for the weights, and a chunk's P goes into
 // columns whose scores have been read. Keys from `seen` on and bad blocks are
-// masked. O's unit 2^u, u = m + v_ref, follows the largest score plus exponent
-// that the row has seen; the first time u is what the tiles before used, which
-// may lie kSpread + 1 above that.
+// masked. O's unit 2^u follows the largest score plus exponent that the row has
+// seen; the first time u is what the tiles before used, which may lie kSpread
+// above that.
 template <int D>
 __device__ __forceinline__ void wide_tile(Bars* sm, int i, int ring, int block_log2, uint32_t s_addr, uint32_t o_addr, float c,
                                           int seen, uint32_t bad, bool have_o, bool first, int lane, float& m, float& l,
-                                          float& v_ref) {
+                                          float& u) {
     const float *ks = sm->k_scale[ring], *vn = sm->v_exp[ring];
     uint32_t s[16];
     auto scores = [&](int k) {
@@ -480,16 +480,13 @@ __device__ __forceinline__ void wide_tile(Bars* sm, int i, int ring, int block_l
         top = fmaxf(top, t * f);
         most = fmaxf(most, t * f + vn[k]);
     }
-    const float to = fmaxf(m, ceilf(top)), was = m + v_ref;
-    const float u = fmaxf(first ? was - (kSpread + 1) : was, ceilf(most));
+    const float to = fmaxf(m, top), was = u;
+    u = fmaxf(first ? u - kSpread : u, most);
     const bool any = to != kNegInf;  // else the row has seen nothing yet: O is 0
     if (have_o) scale_rows<D>(o_addr, any ? ex2_approx(was - u) : 1.0f);
-    const float lift = any ? kLift - to : 0.0f, lift_u = any ? kLift - u : 0.0f;
-    if (any) {
-        l *= ex2_approx(m - to);
-        v_ref = u - to;
-        m = to;
-    }
+    if (any) l *= ex2_approx(m - to);
+    m = to;
+    const float lift = any ? kLift - m : 0.0f, lift_u = any ? kLift - u : 0.0f;
 #pragma unroll 1
     for (int k = 0; k < 8; ++k) {
         const float f = scores(k), e = lift_u + vn[k];
@@ -575,8 +572,10 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
     const uint32_t lanes = (uint32_t)(t >> 5) << 21;  // this warp's TMEM lanes: (t / 32) * 32 << 16
     const uint32_t s_addr = tmem + lanes + i * kKeys, o_addr = tmem + lanes + 2 * kKeys + i * D;
     const int n = w.n[i];
-    // m is a whole number (or -inf), so units change by powers of two. P and l are
-    // in units of 2^(m - kLift), O in units of 2^(m - kLift + r_now).
+    // P and l are in units of 2^(m - kLift), O in units of 2^(m - kLift + r_now). m
+    // is a largest score itself, not rounded: its own weight is then exact in P,
+    // which counts where few keys have most of a row's weight (the error of 26
+    // rows over 32760 keys, scores spread over several units, halves).
     float m = kNegInf, l = 0.0f;
     int r_now = -120;
     bool ok = true;
@@ -636,7 +635,7 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
         }
         if (__builtin_expect(__any_sync(0xffffffffu, tile_top > m + kLazy) || r != r_now, 0)) {
             if (r == kWide) break;  // and so are all tiles behind it
-            const float to = fmaxf(m, ceilf(tile_top));
+            const float to = fmaxf(m, tile_top);
             const float down = to == kNegInf ? 1.0f : ex2_approx(m - to);
             const float fo = down * ex2_approx((float)(r_now - r));
             m = to;
@@ -671,14 +670,18 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
         const float2 t2 = f2_unpack(f2_add(sum[0], sum[1]));
         l += t2.x + t2.y;
     }
-    float v_ref = (float)r_now;  // from here on any number, in place of r_now
-    for (bool first = true; ok && j < n; ++j, first = false) {
-        const int g = dual ? 2 * j + i : j;
-        ok = __all_sync(0xffffffffu, wait_for(&sm->s_full[i], (uint32_t)j & 1u, abort, a.err));
-        if (!ok) break;
-        tc_fence_after();
-        wide_tile<D>(sm, i, g % kRing, a.c.block_log2, s_addr, o_addr, c, limit - g * kKeys,
-                     *(volatile uint32_t*)&sm->bad[g % kRing], j > 0, first, lane, m, l, v_ref);
+    float v_ref = (float)r_now;  // O's unit over l's, log2
+    if (ok && j < n) {
+        float u = m + v_ref;
+        for (bool first = true; j < n; ++j, first = false) {
+            const int g = dual ? 2 * j + i : j;
+            ok = __all_sync(0xffffffffu, wait_for(&sm->s_full[i], (uint32_t)j & 1u, abort, a.err));
+            if (!ok) break;
+            tc_fence_after();
+            wide_tile<D>(sm, i, g % kRing, a.c.block_log2, s_addr, o_addr, c, limit - g * kKeys,
+                         *(volatile uint32_t*)&sm->bad[g % kRing], j > 0, first, lane, m, l, u);
+        }
+        v_ref = m == kNegInf ? 0.0f : u - m;
     }
     // The slot's O; without a key tile the slot's Q, whose buffer takes the rows
     // on their way out: every warp of the slot has to have written its own.

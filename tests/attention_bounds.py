@@ -14,8 +14,8 @@ def attention_seen(q, cache, pages, n, frame, scale, floor="weight"):
 
     With A = sum p |v| per element, over seen keys: p as fp16 is off by half a
     step, 2^-11 of it while normal, else by 2^-25 in units in which the largest
-    p so far is at least 2^6 (the reference is rounded up and a shift of 7 goes
-    on top). So the floor is 2^-31 sum_t r_t 448 S_t, r_t the running maximum
+    p so far is at least 2^6 (2^7, but for what approximate references lose).
+    So the floor is 2^-31 sum_t r_t 448 S_t, r_t the running maximum
     of p over the keys up to the end of t's 128 keys (a later, larger p scales
     the earlier error down with it), S_t the block's scale, which carries codes
     up to 448. Where the block scale is part of p's exponent (floor =
