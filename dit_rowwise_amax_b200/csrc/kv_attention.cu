@@ -22,7 +22,7 @@
 // an 8 x 8 transpose in registers (movmatrix).
 //
 // The products are fp16 (attention.cuh says why; decoding to bf16 this kernel
-// issued 520 instructions per granule instead of 310 and was bound by them).
+// issued 520 instructions per granule instead of 376 and was bound by them).
 // K's scale multiplies the score; V's is in the exponent of P, with a
 // reference m of its own, so P is exact to 2^-32 of the row's largest
 // contribution however V's scales differ. The softmax sum takes a second
@@ -32,7 +32,7 @@
 // and no shuffles.
 //
 // Bound: HBM, 2 bytes per token, kv head and dim. 32 requests of 100 .. 16001
-// tokens, 8 kv heads of 128, 4 query heads each: 103 us, 5.2 TB/s; alone and
+// tokens, 8 kv heads of 128, 4 query heads each: 104 us, 5.1 TB/s; alone and
 // with equal lengths of 8000 the kernel reads 5.7 TB/s (87% of a copy).
 #include <algorithm>
 
@@ -496,18 +496,21 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
 // to kv_attn_rows, 8 or 16 to a CTA; more than that to the tcgen05 kernel, 256
 // to a CTA, unless the keys that kv_attn_rows would walk (once for every 16
 // rows, and a start and an end worth 384 keys) are few, where its shorter start
-// wins: 64 rows x 8 heads over 1024 tokens take 11.0 us there and 17.3 here,
-// x 128 over 128 13.6 and 11.3, x 128 over 2048 73 and 33; 32 x 148 over 256
-// 11.3 and 12.4, over 512 23.6 and 15.5. Over 221 such calls (1 to 148 heads,
-// 17 to 1600 rows, 128 to 4096 tokens) the faster of the two is taken or one
-// 0.6% slower on average, 21% at most.
+// wins: 64 rows x 8 heads over 1024 tokens take 12.3 us there and 19.2 here,
+// x 128 over 128 14.2 and 12.0, x 128 over 2048 74 and 35; 32 x 148 over 256
+// 11.8 and 13.2, over 512 22.7 and 16.3. (The bound comes from 221 such calls,
+// 1 to 148 heads, 17 to 1600 rows, 128 to 4096 tokens: the faster of the two
+// was taken or one 0.6% slower on average, 21% at most.) A request counts at
+// the call's bounds and as seeing all keys: the rule is for requests of equal
+// size; shorter ones and a mask only make CTAs end early.
 // Then the keys are cut into ranges whose results kv_attn_join joins:
 //  - kv_attn_rows: until four CTAs run on every SM (one wave), with ranges of
-//    at least 256 keys and at most kMostRanges of them; beyond one wave, ranges of
-//    about 1024 keys while they are at most 16 CTAs per SM, which even out
-//    requests of different lengths. 16 heads over 1000 tokens take 8.3 us in 4
-//    ranges and 10.8 in 2; 32 x 8 over 4000 50.9 us in 4 ranges, 53.4 in 8 and
-//    59.2 in 2; 32 requests of 100 .. 16001 tokens 103 us in 10, 157 in 2.
+//    at least 256 keys and at most kMostRanges of them; beyond one wave, ranges
+//    of about 1024 keys while they are at most 16 CTAs per SM, which even out
+//    requests of different lengths. 16 heads over 1000 tokens take 8.6 us in 4
+//    ranges and 11.1 in 2; 32 requests of 100 .. 16001 tokens 103 us in 10, 115
+//    in 5, 163 in 2; equal ones pay a little for it: 32 x 8 over 4000 52.5 us in
+//    4 ranges, 49.6 in 2, 53.9 in 1.
 //  - tcgen05 (one CTA per SM): the number of ranges with the earliest estimated
 //    end (tensor_cost).
 //
@@ -515,8 +518,8 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
 // 128 rows fill in after them; a CTA takes 9 us and 1.9 us per tile of 128 keys
 // (a short one 0.83 of that, it decodes every tile for itself), the join reads
 // and writes its partials. For 1560 rows x 16 heads over 32760 tokens it gives
-// 495, 517, 504, 505, 453, 470 us for 1 .. 6 ranges; measured 491, 512, 510,
-// 494, 447, 470.
+// 495, 517, 504, 505, 453, 470 us for 1 .. 6 ranges; measured 491, 504, 493,
+// 480, 441, 477.
 static double tensor_cost(int64_t full, int64_t small, double kv_tiles, double row_bytes, int64_t s, int sms) {
     const double tile = 1.9 * kv_tiles / (double)s, t_full = tile + 9.0, t_small = 0.83 * tile + 9.0;
     full *= s;

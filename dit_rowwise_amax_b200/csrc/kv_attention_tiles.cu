@@ -21,7 +21,7 @@
 // codes and n goes into P's exponent, with a reference per row for O's unit
 // from the keys that the row sees, and the softmax's sum takes a second
 // exponential ("wide" tiles, in a loop of their own: 2.4 times as long, 1560
-// rows x 16 heads over 32760 keys 1060 us instead of 444; 2^14 between two
+// rows x 16 heads over 32760 keys 1040 us instead of 440; 2^14 between two
 // blocks' largest values is rare). Blocks with the smallest scale 2^-120, which
 // blocks of zeros have, do not count for the distance.
 //
@@ -40,12 +40,13 @@
 //
 // Bound: per 256 x 128 tile at dim 128 the MMAs take 2048 cycles and so do the
 // 32768 exponentials at 16 per cycle, and shared memory carries about 2560
-// cycles' worth (raw codes in, decoded tiles out, MMA operands). Measured: 2930
-// cycles per tile, 70% of the tensor pipe; 4096 queries x 8 heads over 16384
-// tokens 1.0 PFLOP/s, 6240 queries x 16 heads over 32760 tokens in frames of
-// 1560 1.37 ms (1.14 PFLOP/s). At dim 64 a tile takes as long (1.79 us as
-// against 1.75): there the softmax's own time bounds it. Loads are far below
-// HBM.
+// cycles' worth (raw codes in, decoded tiles out, MMA operands). Measured: 3550
+// cycles per tile with a CTA's start and end (128 tiles), 68% of the tensor
+// pipe; 4096 queries x 8 heads over 16384 tokens 1.1 PFLOP/s, 6240 queries x
+// 16 heads over 32760 tokens in frames of 1560 1.45 ms (1.07 PFLOP/s at
+// sustained clocks), 32760 queries over as many tokens 6.6 to 7.4 ms (1.33 to
+// 1.19 PFLOP/s). At dim 64 a tile takes as long (1.78 us as against 1.90): there the softmax's
+// own time bounds it. Loads are far below HBM.
 //
 // The running maximum is lazy (attention.cuh), so after the first tiles O stays
 // in TMEM untouched by the softmax threads.

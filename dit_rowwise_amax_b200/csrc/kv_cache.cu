@@ -12,9 +12,10 @@
 // thread keeps 64 of the block's elements (eight 16-byte loads in flight) in
 // registers between the two steps. That is 16 (16 x 64 elements) to 256
 // threads; small blocks put as many heads into a CTA as give it 256, whose
-// slices of a token lie side by side. 32760 tokens, 16 heads of 128: 63 us,
-// 6.4 TB/s (four loads per thread 73.6 us, two 171); blocks of 16 x 64, 12
-// heads, 14441 tokens: 33.6 us with one head per CTA, 11.3 so.
+// slices of a token lie side by side. 32760 tokens, 16 heads of 128: 64 us,
+// 6.3 TB/s (four loads per thread 73.6 us, two 171); seven requests' 10160 new
+// tokens, blocks of 16 x 64, 12 heads: 33.6 us with one head per CTA, 13.3 with
+// whole warps per head, 11.3 so.
 #include <algorithm>
 
 #include "attention.cuh"

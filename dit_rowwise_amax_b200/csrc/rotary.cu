@@ -17,8 +17,8 @@
 // GPU. (Angles taken once per token into shared memory instead: 116 us, the
 // threads' integer divisions and shared reads bound it.) Elements that are
 // only copied go the pairs' way in split order, four and four, so a warp that
-// has both does not load twice in turn (96 of 128 rotated: 24.0 us, 129 us
-// for 32760 tokens).
+// has both does not load twice in turn (96 of 128 rotated, 24 + 8 heads, 4099
+// tokens: 17.1 us; copied eight by eight, loaded in turn: 24.0).
 #include "attention.cuh"
 #include "fp8_codec.cuh"
 

@@ -434,9 +434,10 @@ fp8dit_status fp8_rotary_axes(const fp8dit_heads* q, const fp8dit_heads* k, cons
  * A scale is a power of two: S = 2^n with the smallest n >= -120 for which
  * 448 S >= |x| for every x put into the block. E4M3 keeps its relative
  * precision under any scale, and a power of two makes the quotient x / S, the
- * change of scale when a later token of the block is larger, and code * S in
- * bf16 (what the tensor cores multiply) exact, but for codes that the change
- * of scale makes subnormal, which are rounded once more.
+ * change of scale when a later token of the block is larger, and code * S
+ * exact, but for codes that the change of scale makes subnormal, which are
+ * rounded once more. (The largest bf16 becomes 256 * 2^120, which is infinite
+ * in bf16 and fp32.)
  * head_dim is 64 or 128, block_tokens 16, 32, 64 or 128.
  */
 typedef struct {
@@ -518,7 +519,8 @@ fp8dit_status fp8_kv_cache_append(const fp8dit_kv_cache* cache, const fp8dit_hea
  *   workspace  DEVICE scratch of at least fp8_kv_cache_attention_workspace_size(...) bytes, 16-byte aligned
  *              (may be NULL when that is 0); its contents do not matter, calls that overlap must not share it.
  * Few queries over many tokens: the tokens are split over CTAs and their
- * partial results joined by a second launch; results do not depend on timing.
+ * partial results joined by a second launch. Results do not depend on timing;
+ * the sizes decide on kernel and ranges, which differ by rounding only.
  */
 size_t fp8_kv_cache_attention_workspace_size(const fp8dit_kv_cache* cache, const fp8dit_kv_batch* batch,
                                              int32_t q_heads);
