@@ -68,7 +68,7 @@ struct KvAttnArgs {
     int32_t tail_last;  // 1: the last row tile is a short one and is launched last
     int32_t row_tiles;  // row tiles per request (rows = new tokens x group)
     float* part_o;      // splits > 1: [splits][total * q heads][dim], normalised
-    float* part_lse;    // splits > 1: [splits][total * q heads], log2 units; -inf: no key seen
+    float2* part_sum;   // splits > 1: [splits][total * q heads], reference m (log2 units; -inf: no key seen) and sum of 2^(s - m)
     DevErr err;
 };
 

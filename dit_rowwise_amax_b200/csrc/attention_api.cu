@@ -205,7 +205,7 @@ fp8dit_status fp8_kv_cache_attention(const fp8dit_kv_cache* cache, const fp8dit_
         if (!workspace || !aligned(workspace, 16)) return invalid("this call needs a 16-byte aligned workspace");
         if (ws_bytes < plan.ws_bytes) return invalid("workspace smaller than fp8_kv_cache_attention_workspace_size");
         a.part_o = static_cast<float*>(workspace);
-        a.part_lse = a.part_o + (size_t)plan.splits * (size_t)a.b.total * (size_t)q->heads * (size_t)a.c.dim;
+        a.part_sum = reinterpret_cast<float2*>(a.part_o + (size_t)plan.splits * (size_t)a.b.total * (size_t)q->heads * (size_t)a.c.dim);
     }
     a.q = view(*q), a.out = view(*out);
     a.lse = lse;

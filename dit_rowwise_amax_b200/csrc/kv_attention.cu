@@ -10,7 +10,7 @@
 //
 // Mathematics, per granule and warp (mma.sync m16n8k16, fp16 -> fp32):
 //     S^T = K Q^T      A = 16 keys x dim, B = 8 query rows per column tile
-//     P^T = 2^(7 + t - m)  t = s + log2 S_V: the score plus V's block scale
+//     P^T = 2^(7 + t - v)  t = s - mu + log2 S_V: the score plus V's block scale
 //     O^T += V^T P^T   A = dim x 16 keys, B = P^T
 // Keys and values are the A operands so that 8 rows fill a column tile (the
 // 16-row A side would be half empty at a group of 8 or fewer). Both products
@@ -24,9 +24,10 @@
 // The products are fp16 (attention.cuh says why; decoding to bf16 this kernel
 // issued 520 instructions per granule instead of 376 and was bound by them).
 // K's scale multiplies the score; V's is in the exponent of P, with a
-// reference m of its own, so P is exact to 2^-32 of the row's largest
-// contribution however V's scales differ. The softmax sum takes a second
-// exponential 2^(s - mu), in fp32.
+// reference v of its own (over mu, the scores'), so P is exact to 2^-32 of the
+// row's largest contribution however V's scales differ. The softmax sum takes a
+// second exponential 2^(s - mu), in fp32. Scores only meet as differences, so
+// their size does not matter.
 //
 // Both references are lazy (attention.cuh), so the usual granule needs one vote
 // and no shuffles.
@@ -126,9 +127,20 @@ __device__ __forceinline__ void load_granule(Ring<D>& ring, Header* hdr, int sta
 
 template <int D, int NT>
 struct RowsSmem {
-    float m[kWarps][8 * NT], mu[kWarps][8 * NT], l[kWarps][8 * NT];
+    float v[kWarps][8 * NT], mu[kWarps][8 * NT], l[kWarps][8 * NT];
     float o[kWarps][8 * NT][D + 4];
 };
+
+// The warps' common references of row q: mu, and top for the rest of O's exponent.
+template <int D, int NT>
+__device__ __forceinline__ void common(const RowsSmem<D, NT>& sm, int q, float& mu, float& top) {
+    mu = sm.mu[0][q];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) mu = fmaxf(mu, sm.mu[w][q]);
+    top = kNegInf;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, (sm.mu[w][q] - mu) + sm.v[w][q]);  // NaN without a key: left out
+}
 
 // A warp's running state: per lane the columns (query rows) 2 tig, 2 tig + 1 of
 // every column tile.
@@ -137,7 +149,8 @@ struct RowsState {
     uint32_t q[NT][D / 16][2];  // scaled fp16 Q^T fragments
     float cq[NT][2];            // softmax scale * log2(e) / q's scale
     int limit[NT][2];           // keys the row sees
-    float m[NT][2], mu[NT][2], l[NT][2], o[NT][D / 16][4];
+    float mu[NT][2], v[NT][2];  // references: scores', and of score over mu plus V's exponent
+    float l[NT][2], o[NT][D / 16][4];
 };
 
 template <int D, int NT>
@@ -203,8 +216,8 @@ __device__ __forceinline__ void attend_granule(RowsState<D, NT>& st, const uint8
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float t = fmaxf(s[nt][i], s[nt][i + 2]);
-            over |= t > st.mu[nt][i] + kLazy || t + ev > st.m[nt][i] + kLazy;
+            const float t = fmaxf(s[nt][i], s[nt][i + 2]) - st.mu[nt][i];
+            over |= t > kLazy || t + ev > st.v[nt][i] + kLazy;
         }
     if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
@@ -215,11 +228,14 @@ __device__ __forceinline__ void attend_granule(RowsState<D, NT>& st, const uint8
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
                 t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-                const float mu = fmaxf(st.mu[nt][i], t), m = fmaxf(st.m[nt][i], t + ev);
-                st.l[nt][i] *= mu == kNegInf ? 1.0f : ex2_approx(st.mu[nt][i] - mu);
-                const float c = m == kNegInf ? 1.0f : ex2_approx(st.m[nt][i] - m);
+                const float mu = fmaxf(st.mu[nt][i], t);
+                const bool none = mu == kNegInf;  // nothing seen yet
+                const float down = none ? 0.0f : st.mu[nt][i] - mu, was = st.v[nt][i] + down;
+                const float v = none ? was : fmaxf(was, (t - mu) + ev);
+                st.l[nt][i] *= ex2_approx(down);
+                const float c = ex2_approx(was - v);
                 st.mu[nt][i] = mu;
-                st.m[nt][i] = m;
+                st.v[nt][i] = v;
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
                     st.o[nt][d][i] *= c;
@@ -233,12 +249,12 @@ __device__ __forceinline__ void attend_granule(RowsState<D, NT>& st, const uint8
         float e[4];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            // A row that has seen nothing yet has references of -inf; its scores are too.
-            const float mu = st.mu[nt][i] == kNegInf ? 0.0f : st.mu[nt][i];
-            const float m = (st.m[nt][i] == kNegInf ? 0.0f : st.m[nt][i]) - (ev + kLift);
-            st.l[nt][i] += ex2_approx(s[nt][i] - mu) + ex2_approx(s[nt][i + 2] - mu);
-            e[i] = ex2_approx(s[nt][i] - m);
-            e[i + 2] = ex2_approx(s[nt][i + 2] - m);
+            // A row that has seen nothing yet has a reference of -inf; its scores are too.
+            const float mu = st.mu[nt][i] == kNegInf ? 0.0f : st.mu[nt][i], more = (ev + kLift) - st.v[nt][i];
+            const float d0 = s[nt][i] - mu, d1 = s[nt][i + 2] - mu;
+            st.l[nt][i] += ex2_approx(d0) + ex2_approx(d1);
+            e[i] = ex2_approx(d0 + more);
+            e[i + 2] = ex2_approx(d1 + more);
         }
         p[nt][0] = transpose_8x8(pack_f16x2(e[0], e[1]));
         p[nt][1] = transpose_8x8(pack_f16x2(e[2], e[3]));
@@ -340,7 +356,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3) kv_attn_rows(con
             st.cq[nt][i] = a.scale_log2 * __shfl_sync(0xffffffffu, back, (2 * tig + i) * 4);
             const int lr = r0 + nt * 8 + 2 * tig + i;
             st.limit[nt][i] = lr < rows ? key_limit(r.len - r.n + lr / a.group, r.len, a.frame) : 0;
-            st.m[nt][i] = st.mu[nt][i] = kNegInf;
+            st.mu[nt][i] = kNegInf;
+            st.v[nt][i] = 0.0f;
             st.l[nt][i] = 0.0f;
         }
 #pragma unroll
@@ -376,7 +393,7 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3) kv_attn_rows(con
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             if (gid == 0) {
                 const int q = nt * 8 + 2 * tig + i;
-                sm.m[warp][q] = st.m[nt][i];
+                sm.v[warp][q] = st.v[nt][i];
                 sm.mu[warp][q] = st.mu[nt][i];
                 sm.l[warp][q] = l;
             }
@@ -387,10 +404,9 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3) kv_attn_rows(con
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int q = nt * 8 + 2 * tig + i;
-            float top = sm.m[0][q];
-#pragma unroll
-            for (int w = 1; w < kWarps; ++w) top = fmaxf(top, sm.m[w][q]);
-            const float c = top == kNegInf ? 0.0f : ex2_approx(st.m[nt][i] - top);
+            float mu, top;
+            common<D, NT>(sm, q, mu, top);
+            const float c = st.mu[nt][i] == kNegInf ? 0.0f : ex2_approx((st.mu[nt][i] - mu) + st.v[nt][i] - top);
 #pragma unroll
             for (int d = 0; d < D / 16; ++d) {
                 // Row gid of column tile d is dim gid (D / 8) + 2 d, row gid + 8 the next one.
@@ -404,12 +420,8 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3) kv_attn_rows(con
         const int q = at / (D / 4), d = (at % (D / 4)) * 4;
         const int row = r0 + q;
         if (row >= rows) break;
-        float top = sm.m[0][q], mu = sm.mu[0][q];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) {
-            top = fmaxf(top, sm.m[w][q]);
-            mu = fmaxf(mu, sm.mu[w][q]);
-        }
+        float mu, top;
+        common<D, NT>(sm, q, mu, top);
         float sum = 0.0f;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
@@ -418,28 +430,28 @@ __global__ void __launch_bounds__(32 * kWarps, NT == 1 ? 4 : 3) kv_attn_rows(con
             const float4 y = *reinterpret_cast<const float4*>(&sm.o[w][q][d]);
             x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
         }
-        // out = x 2^(top - kLift - mu) / sum; the power in two steps, it may reach 2^-128.
+        // out = x 2^(top - kLift) / sum; the power in two steps, it may reach 2^-128.
         const bool some = sum > 0.0f || sum != sum;
-        const float half = some ? ex2_approx(0.5f * (top - kLift - mu)) : 0.0f;
+        const float half = some ? ex2_approx(0.5f * (top - kLift)) : 0.0f;
         const float inv = some ? half / sum : 0.0f;
         x.x = x.x * half * inv, x.y = x.y * half * inv, x.z = x.z * half * inv, x.w = x.w * half * inv;
         const int64_t token = r.first + row / a.group;
         const int qh = head * a.group + row % a.group;
         const int64_t flat = token * a.q.heads + qh;
-        const float lse = mu == kNegInf ? kNegInf : mu + lg2_approx(sum);
         if (a.splits > 1) {
             const int64_t part = split * total_rows + flat;
             *reinterpret_cast<float4*>(a.part_o + part * D + d) = x;
-            if (d == 0) a.part_lse[part] = lse;
+            if (d == 0) a.part_sum[part] = make_float2(mu, sum);
         } else {
             *reinterpret_cast<uint2*>(a.out.ptr + token * a.out.token_stride + (int64_t)qh * a.out.head_stride + d) =
                 make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-            if (d == 0 && a.lse) a.lse[flat] = lse * kLog2ToNat;
+            if (d == 0 && a.lse) a.lse[flat] = mu == kNegInf ? kNegInf : kLog2ToNat * (mu + lg2_approx(sum));
         }
     }
 }
 
-// Joins the splits of every row: out = sum_i 2^(lse_i - m) o_i / sum_i 2^(lse_i - m).
+// Joins the splits of every row: out = sum_i w_i o_i / sum_i w_i, w_i = l_i 2^(m_i - max m).
+// (A range's m and sum l come apart: their log2 in one fp32 would lose l beside a large m.)
 // One warp per row, 8 rows per CTA; grid (rows of a request / 8, requests).
 template <int D>
 __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAttnArgs a) {
@@ -455,12 +467,14 @@ __global__ void __launch_bounds__(256) kv_attn_join(const __grid_constant__ KvAt
     // Lane l has the weights of ranges l and l + 32, brought to a sum of one
     // before they meet the ranges' rows: no term is larger than the result may be.
     static_assert(kMostRanges <= 64, "two ranges per lane");
-    const float e0 = lane < n ? a.part_lse[lane * stride + flat] : kNegInf;
-    const float e1 = lane + 32 < n ? a.part_lse[(lane + 32) * stride + flat] : kNegInf;
-    float top = fmaxf(e0, e1);
+    const float2 none = make_float2(kNegInf, 0.0f);
+    const float2 e0 = lane < n ? a.part_sum[lane * stride + flat] : none;
+    const float2 e1 = lane + 32 < n ? a.part_sum[(lane + 32) * stride + flat] : none;
+    float top = fmaxf(e0.x, e1.x);
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-    float w0 = e0 == kNegInf ? 0.0f : ex2_approx(e0 - top), w1 = e1 == kNegInf ? 0.0f : ex2_approx(e1 - top);
+    float w0 = e0.x == kNegInf ? 0.0f : e0.y * ex2_approx(e0.x - top);
+    float w1 = e1.x == kNegInf ? 0.0f : e1.y * ex2_approx(e1.x - top);
     float sum = w0 + w1;
 #pragma unroll
     for (int s = 16; s > 0; s >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, s);

@@ -18,12 +18,12 @@
 // and is brought along when either grows. That is exact while n >= r - 14, and
 // r counts blocks that the mask hides from a row. So from the first tile on
 // after which the exponents met lie more than 14 apart, V is decoded as its
-// codes and n goes into P's exponent, with a reference per row for O's unit
-// from the keys that the row sees, and the softmax's sum takes a second
-// exponential ("wide" tiles, in a loop of their own: 2.4 times as long, 1560
-// rows x 16 heads over 32760 keys 1040 us instead of 440; 2^14 between two
-// blocks' largest values is rare). Blocks with the smallest scale 2^-120, which
-// blocks of zeros have, do not count for the distance.
+// codes ("wide" tiles) and n goes into P's exponent, with a reference per row for
+// O's unit from the keys that the row sees, and the softmax's sum takes a second
+// exponential (careful_tile, in a loop of its own: 2.4 times as long, 1560 rows x
+// 16 heads over 32760 keys 1040 us instead of 440; 2^14 between two blocks'
+// largest values is rare). Blocks with the smallest scale 2^-120, which blocks of
+// zeros have, do not count for the distance.
 //
 // Warp roles (16 warps, one CTA per SM):
 //   0-3, 4-7   softmax of slot 0 and 1, a thread per row. P is handed over in
@@ -45,8 +45,8 @@
 // pipe; 4096 queries x 8 heads over 16384 tokens 1.1 PFLOP/s, 6240 queries x
 // 16 heads over 32760 tokens in frames of 1560 1.45 ms (1.07 PFLOP/s at
 // sustained clocks), 32760 queries over as many tokens 6.6 to 7.4 ms (1.33 to
-// 1.19 PFLOP/s). At dim 64 a tile takes as long (1.78 us as against 1.90): there the softmax's
-// own time bounds it. Loads are far below HBM.
+// 1.19 PFLOP/s). At dim 64 a tile takes as long (1.78 us as against 1.90): there
+// the softmax's own time bounds it. Loads are far below HBM.
 //
 // The running maximum is lazy (attention.cuh), so after the first tiles O stays
 // in TMEM untouched by the softmax threads.
@@ -450,54 +450,65 @@ __device__ __forceinline__ void scale_rows(uint32_t o_addr, float by) {
     }
 }
 
-// A wide tile of slot i, 16 keys at a time: the scores are read from TMEM once
+// A tile of slot i for which the usual loop is not exact: a wide one, or scores
+// so large that a score's product and the rounded reference lie more than the
+// room in P's range apart. 16 keys at a time: the scores are read from TMEM once
 // for the references and once for the weights, and a chunk's P goes into
 // columns whose scores have been read. Keys from `seen` on and bad blocks are
-// masked. O's unit 2^u follows the largest score plus exponent that the row has
-// seen; the first time u is what the tiles before used, which may lie kSpread
-// above that.
+// masked. O is in units of 2^(m + v): v follows the largest score (over m) plus
+// exponent of V that the row has seen; the first time it is what the tiles
+// before used, which may lie kSpread above that. Scores only meet as
+// differences, which are exact where they matter.
 template <int D>
-__device__ __forceinline__ void wide_tile(Bars* sm, int i, int ring, int block_log2, uint32_t s_addr, uint32_t o_addr, float c,
-                                          int seen, uint32_t bad, bool have_o, bool first, int lane, float& m, float& l,
-                                          float& u) {
-    const float *ks = sm->k_scale[ring], *vn = sm->v_exp[ring];
-    uint32_t s[16];
+__device__ __forceinline__ void careful_tile(Bars* sm, int i, int ring, int block_log2, uint32_t s_addr, uint32_t o_addr, float c,
+                                             int seen, uint32_t bad, bool have_o, bool first, int lane, float& m, float& l,
+                                             float& v) {
+    const int r = *(volatile int*)&sm->v_ref[ring];
+    auto unit = [&](int k) { return r == kWide ? sm->v_exp[ring][k] : (float)r; };
+    float s[16];
     auto scores = [&](int k) {
-        tmem_ld_32x32b_x16(s_addr + 16 * k, s);
-        tmem_wait_ld16(s);
+        uint32_t x[16];
+        tmem_ld_32x32b_x16(s_addr + 16 * k, x);
+        tmem_wait_ld16(x);
         const int end = bad >> (16 * k >> block_log2) & 1u ? 0 : seen - 16 * k;
+        const float f = score_factor(c, sm->k_scale[ring][k]);
 #pragma unroll
-        for (int x = 0; x < 16; ++x)
-            if (x >= end) s[x] = __float_as_uint(kNegInf);
-        return score_factor(c, ks[k]);
+        for (int y = 0; y < 16; ++y) s[y] = y < end ? __fmul_rn(__uint_as_float(x[y]), f) : kNegInf;
     };
-    float top = kNegInf, most = kNegInf;
-#pragma unroll 1
-    for (int k = 0; k < 8; ++k) {
-        const float f = scores(k);
-        float t = __uint_as_float(s[0]);
+    float t[8], top = kNegInf;
 #pragma unroll
-        for (int x = 1; x < 16; ++x) t = fmaxf(t, __uint_as_float(s[x]));
-        top = fmaxf(top, t * f);
-        most = fmaxf(most, t * f + vn[k]);
+    for (int k = 0; k < 8; ++k) {
+        scores(k);
+        t[k] = s[0];
+#pragma unroll
+        for (int x = 1; x < 16; ++x) t[k] = fmaxf(t[k], s[x]);
+        top = fmaxf(top, t[k]);
     }
-    const float to = fmaxf(m, top), was = u;
-    u = fmaxf(first ? u - kSpread : u, most);
+    const float to = fmaxf(m, top);
     const bool any = to != kNegInf;  // else the row has seen nothing yet: O is 0
-    if (have_o) scale_rows<D>(o_addr, any ? ex2_approx(was - u) : 1.0f);
-    if (any) l *= ex2_approx(m - to);
-    m = to;
-    const float lift = any ? kLift - m : 0.0f, lift_u = any ? kLift - u : 0.0f;
+    float scale_o = 1.0f;
+    if (any) {
+        const float down = m - to;
+        float next = (first ? v - kSpread : v) + down;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) next = fmaxf(next, (t[k] - to) + unit(k));
+        l *= ex2_approx(down);
+        scale_o = ex2_approx(v + down - next);
+        v = next, m = to;
+    }
+    if (have_o) scale_rows<D>(o_addr, scale_o);
+    const float ref = any ? m : 0.0f;
 #pragma unroll 1
     for (int k = 0; k < 8; ++k) {
-        const float f = scores(k), e = lift_u + vn[k];
+        scores(k);
+        const float more = unit(k) - v;
         float sum = 0.0f;
         uint32_t p[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-            const float s0 = __uint_as_float(s[2 * x]), s1 = __uint_as_float(s[2 * x + 1]);
-            sum += ex2_approx(fmaf(s0, f, lift)) + ex2_approx(fmaf(s1, f, lift));
-            p[x] = pack_f16x2(ex2_approx(fmaf(s0, f, e)), ex2_approx(fmaf(s1, f, e)));
+            const float d0 = (s[2 * x] - ref) + kLift, d1 = (s[2 * x + 1] - ref) + kLift;
+            sum += ex2_approx(d0) + ex2_approx(d1);
+            p[x] = pack_f16x2(ex2_approx(d0 + more), ex2_approx(d1 + more));
         }
         tmem_st_32x32b_x8(s_addr + 8 * k, p);
         l += sum;
@@ -638,7 +649,9 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
             tile_top = fmaxf(tile_top, fmaxf(u0, u1) * f[z]);
         }
         if (__builtin_expect(__any_sync(0xffffffffu, tile_top > m + kLazy) || r != r_now, 0)) {
-            if (r == kWide) {  // and so are all tiles behind it
+            // From here on the careful way: wide (as are all tiles behind it), or
+            // scores of 2^22 and more.
+            if (r == kWide || __any_sync(0xffffffffu, fabsf(tile_top) > 0x1p22f && tile_top != kNegInf)) {
                 recent = 0.0f;
                 break;
             }
@@ -679,17 +692,13 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
     }
     l += recent;
     float v_ref = (float)r_now;  // O's unit over l's, log2
-    if (ok && j < n) {
-        float u = m + v_ref;
-        for (bool first = true; j < n; ++j, first = false) {
-            const int g = dual ? 2 * j + i : j;
-            ok = __all_sync(0xffffffffu, wait_for(&sm->s_full[i], (uint32_t)j & 1u, abort, a.err));
-            if (!ok) break;
-            tc_fence_after();
-            wide_tile<D>(sm, i, g % kRing, a.c.block_log2, s_addr, o_addr, c, limit - g * kKeys,
-                         *(volatile uint32_t*)&sm->bad[g % kRing], j > 0, first, lane, m, l, u);
-        }
-        v_ref = m == kNegInf ? 0.0f : u - m;
+    for (bool first = true; ok && j < n; ++j, first = false) {
+        const int g = dual ? 2 * j + i : j;
+        ok = __all_sync(0xffffffffu, wait_for(&sm->s_full[i], (uint32_t)j & 1u, abort, a.err));
+        if (!ok) break;
+        tc_fence_after();
+        careful_tile<D>(sm, i, g % kRing, a.c.block_log2, s_addr, o_addr, c, limit - g * kKeys,
+                        *(volatile uint32_t*)&sm->bad[g % kRing], j > 0, first, lane, m, l, v_ref);
     }
     // The slot's O; without a key tile the slot's Q, whose buffer takes the rows
     // on their way out: every warp of the slot has to have written its own.
@@ -752,11 +761,10 @@ __device__ __forceinline__ void softmax_role(const KvAttnArgs& a, Bars* sm, uint
     const int64_t flat = tok * a.q.heads + qh;
     const int64_t part = (int64_t)w.split * a.b.total * a.q.heads + flat;
     if (in) {
-        const float lse = m == kNegInf ? kNegInf : m - kLift + lg2_approx(l);
         if (a.splits > 1)
-            a.part_lse[part] = lse;
+            a.part_sum[part] = make_float2(m, l * (1.0f / (1 << (int)kLift)));
         else if (a.lse)
-            a.lse[flat] = lse * kLog2ToNat;
+            a.lse[flat] = m == kNegInf ? kNegInf : kLog2ToNat * (m - kLift + lg2_approx(l));
     }
     // Through the slot's Q buffer (all four warps have written it, every product
     // with it is done), so that rows leave in whole lines: 16-byte pieces,
