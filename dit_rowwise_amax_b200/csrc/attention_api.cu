@@ -71,6 +71,14 @@ fp8dit_status check_batch(const fp8dit_kv_batch* b, const KvCacheView& c, KvBatc
 
 bool nothing(const KvBatchView& b) { return b.n == 0 || b.total == 0 || b.max_new == 0; }
 
+// Query heads over a cache, and the bound that keeps the plan's numbers in 32 bits.
+fp8dit_status check_q_heads(int32_t q_heads, const KvCacheView& c, const KvBatchView& b) {
+    if (q_heads <= 0 || q_heads % c.heads != 0) return invalid("q's heads must be a multiple of the cache's");
+    if (q_heads > kMaxHeads) return unsupported("too many query heads");
+    if (!nothing(b) && (int64_t)b.max_new * q_heads > INT32_MAX) return unsupported("max_new x heads too large");
+    return FP8DIT_OK;
+}
+
 }  // namespace
 }  // namespace fp8dit
 
@@ -150,8 +158,9 @@ size_t fp8_kv_cache_attention_workspace_size(const fp8dit_kv_cache* cache, const
     clear_error();
     KvCacheView c{};
     KvBatchView b{};
-    if (check_cache(cache, &c) != FP8DIT_OK || check_batch(batch, c, &b) != FP8DIT_OK) return 0;
-    if (q_heads <= 0 || q_heads % c.heads != 0 || nothing(b)) return 0;
+    if (check_cache(cache, &c) != FP8DIT_OK || check_batch(batch, c, &b) != FP8DIT_OK ||
+        check_q_heads(q_heads, c, b) != FP8DIT_OK || nothing(b))
+        return 0;
     const DeviceInfo* dev = device_info();
     return dev ? kv_attn_plan(c, b, q_heads, dev->num_sms).ws_bytes : 0;
 }
@@ -163,8 +172,8 @@ fp8dit_status fp8_kv_cache_attention_plan(const fp8dit_kv_cache* cache, const fp
     KvBatchView b{};
     fp8dit_status st = check_cache(cache, &c);
     if (st == FP8DIT_OK) st = check_batch(batch, c, &b);
+    if (st == FP8DIT_OK) st = check_q_heads(q_heads, c, b);
     if (st != FP8DIT_OK) return st;
-    if (q_heads <= 0 || q_heads % c.heads != 0) return invalid("q's heads must be a multiple of the cache's");
     KvAttnPlan plan{};
     if (!nothing(b)) {
         const DeviceInfo* dev = device_info();
@@ -185,8 +194,7 @@ fp8dit_status fp8_kv_cache_attention(const fp8dit_kv_cache* cache, const fp8dit_
     if (st == FP8DIT_OK) st = check_batch(batch, a.c, &a.b);
     if (st != FP8DIT_OK) return st;
     if (!q || !out) return invalid("null tensor description");
-    if (q->heads <= 0 || q->heads % a.c.heads != 0) return invalid("q's heads must be a multiple of the cache's");
-    if (q->heads > kMaxHeads) return unsupported("too many query heads");
+    if ((st = check_q_heads(q->heads, a.c, a.b)) != FP8DIT_OK) return st;
     if (out->heads != q->heads) return invalid("out's heads differ from q's");
     const float scale_log2 = scale * 1.4426950408889634f;
     if (!(scale > 0.0f) || !std::isfinite(scale_log2)) return invalid("scale must be > 0 and finite, times log2(e) too");
@@ -195,7 +203,6 @@ fp8dit_status fp8_kv_cache_attention(const fp8dit_kv_cache* cache, const fp8dit_
     for (const fp8dit_heads* x : {q, out})
         if (const char* msg = heads_problem(*x, a.c.dim)) return invalid(msg);
     if (!aligned(lse, 4)) return invalid("lse must be 4-byte aligned");
-    if ((int64_t)a.b.max_new * q->heads > INT32_MAX) return unsupported("max_new x heads too large");
     const DeviceInfo* dev = device_info();
     if (!dev) return FP8DIT_ERR_CUDA;
     const KvAttnPlan plan = kv_attn_plan(a.c, a.b, q->heads, dev->num_sms);

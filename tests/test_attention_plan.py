@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import dit_rowwise_amax_b200 as fp8
-from test_attention_args import BATCH, CACHE, INVALID, OK, batch, cache
+from test_attention_args import BATCH, CACHE, INVALID, OK, UNSUPPORTED, batch, cache
 
 
 @pytest.fixture(scope="module")
@@ -55,3 +55,18 @@ def test_plan_agrees_with_the_workspace(requests, new, heads, kv, cached):
     desc = fp8._kv_batch(table, lens, offsets, requests * new, new, cached, 128, q.device)
     need = fp8.load_library().fp8_kv_cache_attention_workspace_size(fp8._kv_cache(c)[0], desc, heads)
     assert 1 <= ranges <= 64 and (need > 0) == (ranges > 1)
+
+
+@pytest.mark.parametrize("q_heads,max_new", [(1 << 16, 2), (1 << 20, 1 << 20), (1 << 30, 1 << 30), (4, 1 << 29)])
+def test_sizes_that_the_call_refuses_have_no_plan_and_no_workspace(lib, q_heads, max_new):
+    b = batch(max_new=max_new, total=1 << 30)
+    assert plan(lib, cache(kv_heads=1), b, q_heads)[0] == UNSUPPORTED
+    assert lib.fp8_kv_cache_attention_workspace_size(cache(kv_heads=1), b, q_heads) == 0
+    assert lib.fp8dit_last_error_string() != b""
+
+
+def test_a_call_of_nothing_may_have_any_bound(lib):
+    empty = batch(max_new=1 << 30, total=0)
+    assert plan(lib, cache(kv_heads=1), empty, 4) == (OK, 0, 0)
+    c, q = cache(), fp8._Heads(None, 256, 64, 4, 0)
+    assert lib.fp8_kv_cache_attention(c, q, empty, q, None, 0.125, 0, None, 0, None) == OK
