@@ -20,8 +20,8 @@
 // after which the exponents met lie more than 14 apart, V is decoded as its
 // codes ("wide" tiles) and n goes into P's exponent, with a reference per row for
 // O's unit from the keys that the row sees, and the softmax's sum takes a second
-// exponential (careful_tile, in a loop of its own: 2.4 times as long, 1560 rows x
-// 16 heads over 32760 keys 1040 us instead of 440; 2^14 between two blocks'
+// exponential (careful_tile, in a loop of its own: 2.6 times as long, 1560 rows x
+// 16 heads over 32760 keys 1120 us instead of 430; 2^14 between two blocks'
 // largest values is rare). Blocks with the smallest scale 2^-120, which blocks of
 // zeros have, do not count for the distance.
 //
